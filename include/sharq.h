@@ -504,6 +504,150 @@ sharq_status sharq_linear_grouped(const sharq_prep *prep, const int32_t *offsets
                                   int64_t rows, const sharq_wq *wq, void *out_dev, void *stream);
 
 /*
+ * Operators around the FP4 linear in 16 or 32 bits.
+ *
+ * Interface additions: the SharQ abstract describes the linear only. These
+ * are what a model needs next to it: the normalization as an operator of its
+ * own (sharq_prepare normalizes inside and never writes the normalized rows)
+ * with its backward pass, low-rank adapters beside a shared projection, and
+ * the token order of mixture-of-experts layers.
+ *
+ * Element types are a sharq_dtype. Values are widened to binary32, sums are
+ * binary32 in a fixed order (the same inputs give the same bits), and results
+ * are rounded once to the element type. Matrices are row-major and
+ * contiguous unless a row stride (ld*, in elements) is given. Buffers need the
+ * alignment of their elements; rows of a multiple of 16 bytes in 16-byte
+ * aligned buffers take the fast path. Outputs must not overlap inputs except
+ * where a comment allows it (SHARQ_ERR_INVALID_ARG). Calls with no rows
+ * enqueue nothing unless a comment says otherwise. Sizes: 1 <= k <=
+ * SHARQ_K_MAX, 0 <= m_tok <= 2^30 unless stated.
+ */
+typedef enum sharq_dtype {
+    SHARQ_F16 = 0,
+    SHARQ_BF16 = 1,
+    SHARQ_F32 = 2
+} sharq_dtype;
+
+/*
+ * LayerNorm (norm = 0) or RMSNorm (norm = 1) of x [m_tok][k]:
+ *   y = (x - mean) * rstd * ln_w + ln_b,  rstd = 1 / sqrt(var + eps)
+ * with mean = 0 and var the mean square for RMSNorm (ln_b NULL there).
+ *   ln_w_dev, ln_b_dev  [k] of the element type, or NULL.
+ *   mean_dev, rstd_dev  float [m_tok] for the backward pass, or NULL (mean_dev
+ *                       is NULL for RMSNorm).
+ *   eps                 finite and > 0.
+ * The statistics are binary32 sums, the variance around the mean. They are
+ * not the exact statistics of sharq_prepare, which differ in the last bits.
+ */
+sharq_status sharq_layer_norm(const void *x_dev, int64_t m_tok, int64_t k, const void *ln_w_dev, const void *ln_b_dev,
+                              float eps, int norm, int dtype, void *y_dev, float *mean_dev, float *rstd_dev,
+                              void *stream);
+
+/*
+ * Backward pass of sharq_layer_norm. With xhat = (x - mean) rstd, g = dy ln_w
+ * (dy where ln_w is NULL) and means over k:
+ *   dx = rstd * (g - mean(g) - xhat * mean(g * xhat))   (RMSNorm: no mean(g))
+ *   dw = sum over rows of dy * xhat,  db = sum over rows of dy
+ *   mean_dev, rstd_dev  the forward pass's statistics (mean_dev NULL for
+ *                       RMSNorm).
+ *   dx_dev              [m_tok][k] of the element type; may be dy_dev itself.
+ *   dw_dev, db_dev      float [k], or NULL; written (zero) for m_tok == 0 too.
+ *   ws_dev              workspace of sharq_layer_norm_backward_bytes(m_tok, k)
+ *                       bytes, 256-byte aligned; NULL if dw and db are NULL.
+ */
+size_t sharq_layer_norm_backward_bytes(int64_t m_tok, int64_t k);
+sharq_status sharq_layer_norm_backward(const void *dy_dev, const void *x_dev, int64_t m_tok, int64_t k,
+                                       const void *ln_w_dev, const float *mean_dev, const float *rstd_dev, int norm,
+                                       int dtype, void *dx_dev, float *dw_dev, float *db_dev, void *ws_dev,
+                                       size_t ws_bytes, void *stream);
+
+/* Most choices per token, and most rank, of the calls below. */
+#define SHARQ_TOP_K_MAX 64
+#define SHARQ_RANK_MAX 128
+
+/*
+ * Entries sorted by group: entry (t, j) is choice j of token t and belongs to
+ * group ids[t][j]; an id outside 0 .. n_groups-1 (such as -1: a padding token,
+ * a request without an adapter) belongs to none. A stable counting sort in one
+ * launch:
+ *   ids_dev      [m_tok][top_k], int32 (id_bytes = 4) or int64 (id_bytes = 8).
+ *   offsets_dev  int32 [n_groups + 1]: group g's grouped rows are offsets[g] ..
+ *                offsets[g+1] - 1, in the order of their entries.
+ *   rows_dev     int32 [m_tok * top_k]: the token of each grouped row; -1 behind
+ *                the last group.
+ *   slots_dev    int32 [m_tok][top_k]: the grouped row of each entry, -1 for
+ *                entries without a group.
+ * offsets and rows are the routing arrays of sharq_gather_rows and
+ * sharq_prepare_grouped (which need offsets[n_groups] == rows, so every entry
+ * in a group). 1 <= n_groups <= SHARQ_GROUPS_MAX, 1 <= top_k <=
+ * SHARQ_TOP_K_MAX, m_tok * top_k <= 2^30; m_tok == 0 writes the offsets.
+ */
+sharq_status sharq_route(const void *ids_dev, int id_bytes, int64_t m_tok, int64_t top_k, int64_t n_groups,
+                         int32_t *offsets_dev, int32_t *rows_dev, int32_t *slots_dev, void *stream);
+
+/*
+ * Rows into grouped order: out[slots[t][j]] = x[t] for every entry with a
+ * slot, and zero rows from offsets[n_groups] on. out_dev [m_tok * top_k][k];
+ * x_dev [m_tok][k]. The gradient of this is sharq_combine without weights.
+ * Slots >= m_tok * top_k are skipped and reported (sharq_get_last_error:
+ * SHARQ_ERR_INVALID_ARG); two entries with one slot leave either's row there.
+ */
+sharq_status sharq_permute_rows(const void *x_dev, int64_t m_tok, int64_t k, const int32_t *slots_dev, int64_t top_k,
+                                const int32_t *offsets_dev, int64_t n_groups, int dtype, void *out_dev, void *stream);
+
+/*
+ * Grouped rows back to their tokens:
+ *   out[t] = residual[t] + sum_j weights[t][j] * y[slots[t][j]]
+ * over the entries with a slot.
+ *   y_dev         [rows][k] in grouped order.
+ *   weights_dev   float [m_tok][top_k], or NULL (all 1).
+ *   residual_dev  [m_tok][k] or NULL; out_dev may be residual_dev itself.
+ * Slots >= rows are skipped and reported as in sharq_permute_rows.
+ */
+sharq_status sharq_combine(const void *y_dev, int64_t rows, int64_t m_tok, int64_t k, const int32_t *slots_dev,
+                           const float *weights_dev, int64_t top_k, const void *residual_dev, int dtype, void *out_dev,
+                           void *stream);
+
+/*
+ * Backward pass of sharq_combine (the residual's gradient is dout itself):
+ *   dy[slots[t][j]] = weights[t][j] * dout[t], zero rows from
+ *   offsets[n_groups] on;  dweights[t][j] = <dout[t], y[slots[t][j]]>, 0 for
+ *   entries without a slot.
+ * dy_dev [rows][k] of the element type, dweights_dev float [m_tok][top_k].
+ */
+sharq_status sharq_combine_backward(const void *dout_dev, const void *y_dev, int64_t rows, int64_t m_tok, int64_t k,
+                                    const int32_t *slots_dev, const float *weights_dev, int64_t top_k,
+                                    const int32_t *offsets_dev, int64_t n_groups, int dtype, void *dy_dev,
+                                    float *dweights_dev, void *stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection:
+ *   out[r] = base[r] + scales[g] * (x[r] A[g]^T) B[g]^T
+ * where g is row r's group; rows without a group get base[r]. base is the
+ * shared projection's output (sharq_linear's, for instance).
+ *   x_dev     [m_tok][k], row stride ldx.
+ *   a_dev     [n_groups][rank][k], b_dev [n_groups][n_out][rank], contiguous.
+ *             Adapters of a smaller rank are padded with zeros.
+ *   scales_dev  float [n_groups], or NULL (all 1).
+ *   offsets_dev, rows_dev, slots_dev  from sharq_route with top_k = 1.
+ *   base_dev  [m_tok][n_out], row stride ldbase, or NULL (zero).
+ *   out_dev   [m_tok][n_out], row stride ldo; may be base_dev itself (ldo ==
+ *             ldbase), then rows without a group are left alone.
+ * The product x A^T is kept in binary32 (each row as two 16-bit terms for the
+ * second product), accumulation is binary32, the sum is rounded once.
+ * dtype is SHARQ_F16 or SHARQ_BF16. k, n_out, rank and the row strides are
+ * multiples of 8, buffers 16-byte aligned; rank <= SHARQ_RANK_MAX, n_out <=
+ * 2^20, n_groups <= SHARQ_GROUPS_MAX. Column slices of one buffer are fine as
+ * x, base or out where their columns are disjoint.
+ * Invalid offsets write nothing, invalid rows are skipped; both are reported
+ * by sharq_get_last_error as SHARQ_ERR_INVALID_ARG.
+ */
+sharq_status sharq_lora(const void *x_dev, int64_t ldx, int64_t m_tok, int64_t k, const void *a_dev, const void *b_dev,
+                        int64_t n_out, int64_t rank, int64_t n_groups, const float *scales_dev,
+                        const int32_t *offsets_dev, const int32_t *rows_dev, const int32_t *slots_dev, int dtype,
+                        const void *base_dev, int64_t ldbase, void *out_dev, int64_t ldo, void *stream);
+
+/*
  * Canonical host copies of a prepared activation, for inspection and tests.
  * Synchronizes `stream`. Every output may be NULL. One value per byte:
  *   idx_host      [m_tok][k/m][n] kept positions, ascending

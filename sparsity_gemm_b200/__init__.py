@@ -103,6 +103,15 @@ def lib():
         L.sharq_weight_bytes_sparse.argtypes = [i64, i64, i32]
         L.sharq_weight_bytes_sparse.restype = sz
         L.sharq_quantize_weight_sparse.argtypes = [vp, i64, i64, i32, vp, sz, C.POINTER(SharqWQ), vp]
+        L.sharq_layer_norm.argtypes = [vp, i64, i64, vp, vp, f32, i32, i32, vp, vp, vp, vp]
+        L.sharq_layer_norm_backward_bytes.argtypes = [i64, i64]
+        L.sharq_layer_norm_backward_bytes.restype = sz
+        L.sharq_layer_norm_backward.argtypes = [vp, vp, i64, i64, vp, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp]
+        L.sharq_route.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp]
+        L.sharq_permute_rows.argtypes = [vp, i64, i64, vp, i64, vp, i64, i32, vp, vp]
+        L.sharq_combine.argtypes = [vp, i64, i64, i64, vp, vp, i64, vp, i32, vp, vp]
+        L.sharq_combine_backward.argtypes = [vp, vp, i64, i64, i64, vp, vp, i64, vp, i64, i32, vp, vp, vp]
+        L.sharq_lora.argtypes = [vp, i64, i64, i64, vp, vp, i64, i64, i64, vp, vp, vp, vp, i32, vp, i64, vp, i64, vp]
         L.sharq_status_string.argtypes = [i32]
         L.sharq_status_string.restype = C.c_char_p
         L.sharq_last_launch_count.restype = i32
@@ -110,7 +119,9 @@ def lib():
                      "sharq_weight_export", "sharq_get_last_error", "sharq_quantize_weight_grouped",
                      "sharq_gather_rows", "sharq_linear_grouped", "sharq_prepare_rms",
                      "sharq_quantize_weight_fused", "sharq_linear_bias", "sharq_weight_tensor_scales",
-                     "sharq_prepare_grouped", "sharq_prepare_sparse", "sharq_quantize_weight_sparse", "sharq_prepare_add"):
+                     "sharq_prepare_grouped", "sharq_prepare_sparse", "sharq_quantize_weight_sparse", "sharq_prepare_add",
+                     "sharq_layer_norm", "sharq_layer_norm_backward", "sharq_route", "sharq_permute_rows",
+                     "sharq_combine", "sharq_combine_backward", "sharq_lora"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -522,6 +533,267 @@ def linear_grouped(prep: Prepared, offsets: torch.Tensor, qw: QuantizedWeight, r
     optr = _ptr(out) if out.numel() else None
     _check(lib().sharq_linear_grouped(C.byref(prep.desc), _ptr(offsets), offsets.numel() - 1, rows, C.byref(qw.desc),
                                       optr, _stream(stream)), "sharq_linear_grouped")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Operators around the FP4 linear in 16 or 32 bits
+
+F16, BF16, F32 = 0, 1, 2
+TOP_K_MAX, RANK_MAX, GROUPS_MAX = 64, 128, 1024
+_DTYPES = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _matrix(t: torch.Tensor, name: str, dtype=None, shape=None, strided: bool = False):
+    """t is a CUDA matrix of a supported type (of `dtype` and `shape` where
+    given): contiguous, or with rows of consecutive elements if strided."""
+    _require(isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in _DTYPES,
+             f"{name} must be an fp16, bf16 or fp32 matrix")
+    _require(dtype is None or t.dtype == dtype, f"{name} must be of type {dtype}")
+    _require(shape is None or tuple(t.shape) == tuple(shape), f"{name} must have the shape {tuple(shape or ())}")
+    if strided:
+        _require(t.numel() == 0 or ((t.stride(1) == 1 or t.shape[1] == 1)
+                                    and (t.stride(0) >= t.shape[1] or t.shape[0] == 1)),
+                 f"the rows of {name} must hold consecutive elements and not overlap")
+    else:
+        _require(t.is_contiguous(), f"{name} must be contiguous")
+    _cuda_here(t, name)
+
+
+def _vector(t: torch.Tensor, name: str, dtype, n: int):
+    _require(isinstance(t, torch.Tensor) and t.dtype == dtype and t.dim() == 1 and t.is_contiguous() and t.numel() == n,
+             f"{name} must be a contiguous vector of {n} elements of type {dtype}")
+    _cuda_here(t, name)
+
+
+def _no_grad_inputs(*ts):
+    """The calls below are not recorded by autograd; a call that would lose a
+    gradient silently is refused (the *_backward calls are the gradients)."""
+    _require(not (torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in ts)),
+             "inputs that require a gradient are refused: call under torch.no_grad() and use the backward calls")
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream its kernel runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride in elements (a single row has none of its own)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def layer_norm(x: torch.Tensor, w=None, b=None, eps: float = 1e-5, norm: str = "layer", stats: bool = False,
+               out: torch.Tensor | None = None, stream=None):
+    """LayerNorm (norm="layer", weight w, bias b) or RMSNorm (norm="rms", no
+    b) of x [m_tok, k] (fp16, bf16 or fp32): x's type, rounded once. With
+    stats=True returns (y, mean, rstd) for layer_norm_backward: fp32 [m_tok],
+    mean None for RMSNorm."""
+    _require(norm in ("layer", "rms") and (norm == "layer" or b is None),
+             'norm must be "layer" or "rms" (RMSNorm takes no b)')
+    _matrix(x, "x")
+    m_tok, k = x.shape
+    for t, name in ((w, "w"), (b, "b")):
+        if t is not None:
+            _vector(t, name, x.dtype, k)
+    _no_grad_inputs(x, w, b)
+    if out is None:
+        out = _empty((m_tok, k), x.dtype, x.device, stream)
+    _matrix(out, "out", x.dtype, x.shape)
+    mean = _empty((m_tok,), torch.float32, x.device, stream) if stats and norm == "layer" else None
+    rstd = _empty((m_tok,), torch.float32, x.device, stream) if stats else None
+    _check(lib().sharq_layer_norm(_ptr(x), m_tok, k, _ptr(w), _ptr(b), float(eps), 1 if norm == "rms" else 0,
+                                  _DTYPES[x.dtype], _ptr(out), _ptr(mean), _ptr(rstd), _stream(stream)),
+           "sharq_layer_norm")
+    return (out, mean, rstd) if stats else out
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean, rstd: torch.Tensor, w=None, norm: str = "layer",
+                        out: torch.Tensor | None = None, stream=None):
+    """Gradients of layer_norm: (dx, dw, db) from dy and the forward pass's x,
+    mean (None for RMSNorm), rstd and w. dx has x's type (out: where to put it,
+    may be dy itself); dw and db are fp32 [k], None without w, and db None for
+    RMSNorm."""
+    _require(norm in ("layer", "rms") and (norm == "layer") == (mean is not None),
+             'norm must be "layer" (with mean) or "rms" (mean None)')
+    _matrix(x, "x")
+    _matrix(dy, "dy", x.dtype, x.shape)
+    m_tok, k = x.shape
+    if mean is not None:
+        _vector(mean, "mean", torch.float32, m_tok)
+    _vector(rstd, "rstd", torch.float32, m_tok)
+    if w is not None:
+        _vector(w, "w", x.dtype, k)
+    _no_grad_inputs(dy, x, w)
+    if out is None:
+        out = _empty((m_tok, k), x.dtype, x.device, stream)
+    _matrix(out, "out", x.dtype, x.shape)
+    dw = db = ws = None
+    nbytes = 0
+    if w is not None:
+        nbytes = int(lib().sharq_layer_norm_backward_bytes(m_tok, k))
+        if nbytes == 0:
+            raise SharqError(ERR_INVALID_ARG, f"layer_norm_backward shape {tuple(x.shape)}")
+        dw = _empty((k,), torch.float32, x.device, stream)
+        db = _empty((k,), torch.float32, x.device, stream) if norm == "layer" else None
+        ws = _empty((nbytes,), torch.uint8, x.device, stream)
+    _check(lib().sharq_layer_norm_backward(_ptr(dy), _ptr(x), m_tok, k, _ptr(w), _ptr(mean), _ptr(rstd),
+                                           1 if norm == "rms" else 0, _DTYPES[x.dtype], _ptr(out), _ptr(dw), _ptr(db),
+                                           _ptr(ws), nbytes, _stream(stream)), "sharq_layer_norm_backward")
+    return out, dw, db
+
+
+class Routing:
+    """Entries sorted by group (route): int32 CUDA tensors offsets [groups +
+    1], rows [m_tok * top_k] (the token of each grouped row, -1 behind the
+    last group) and slots [m_tok, top_k] (the grouped row of each entry, -1:
+    none). Made once, it serves every call of the step that sorts by the same
+    ids."""
+
+    def __init__(self, offsets: torch.Tensor, rows: torch.Tensor, slots: torch.Tensor):
+        _int32_vector(offsets, "offsets")
+        _int32_vector(rows, "rows")
+        _require(isinstance(slots, torch.Tensor) and slots.dtype == torch.int32 and slots.dim() == 2
+                 and slots.is_contiguous(), "slots must be a contiguous int32 matrix")
+        _cuda_here(slots, "slots")
+        _require(offsets.numel() >= 2 and rows.numel() == slots.numel() and slots.shape[1] >= 1,
+                 "rows must hold one element per element of slots, offsets one more than there are groups")
+        self.offsets, self.rows, self.slots = offsets, rows, slots
+
+    @property
+    def groups(self) -> int:
+        return self.offsets.numel() - 1
+
+    @property
+    def m_tok(self) -> int:
+        return self.slots.shape[0]
+
+    @property
+    def top_k(self) -> int:
+        return self.slots.shape[1]
+
+
+def _routing(r, m_tok=None):
+    _require(isinstance(r, Routing), "routing must be a Routing (from route)")
+    _cuda_here(r.offsets, "routing.offsets")
+    _require(m_tok is None or r.m_tok == m_tok, f"routing is of {r.m_tok} tokens, not {m_tok}")
+
+
+def route(ids: torch.Tensor, groups: int, stream=None) -> Routing:
+    """Entries sorted by group, on the GPU: ids [m_tok, top_k] (or [m_tok]),
+    int32 or int64, holds each entry's expert or adapter; an id outside 0 ..
+    groups - 1 (-1, say) means none. Entries of a group keep their order."""
+    _require(isinstance(ids, torch.Tensor) and ids.dtype in (torch.int32, torch.int64) and ids.dim() in (1, 2)
+             and ids.is_contiguous(), "ids must be a contiguous int32 or int64 matrix (or vector)")
+    _cuda_here(ids, "ids")
+    m_tok, top_k = ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1
+    _require(1 <= top_k <= TOP_K_MAX and 1 <= groups <= GROUPS_MAX,
+             f"route takes 1 to {TOP_K_MAX} ids per token and 1 to {GROUPS_MAX} groups")
+    r = Routing(_empty((groups + 1,), torch.int32, ids.device, stream),
+                _empty((m_tok * top_k,), torch.int32, ids.device, stream),
+                _empty((m_tok, top_k), torch.int32, ids.device, stream))
+    _check(lib().sharq_route(_ptr(ids), ids.element_size(), m_tok, top_k, groups, _ptr(r.offsets), _ptr(r.rows),
+                             _ptr(r.slots), _stream(stream)), "sharq_route")
+    return r
+
+
+def permute_rows(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rows of x [m_tok, k] in grouped order: [m_tok * top_k, k], row
+    slots[t, j] = x[t], zero behind the last group (what prepare_grouped and
+    the grouped products read). Its gradient is combine(dy, routing)."""
+    _matrix(x, "x")
+    _routing(routing, x.shape[0])
+    _no_grad_inputs(x)
+    shape = (routing.rows.numel(), x.shape[1])
+    if out is None:
+        out = _empty(shape, x.dtype, x.device, stream)
+    _matrix(out, "out", x.dtype, shape)
+    _check(lib().sharq_permute_rows(_ptr(x), x.shape[0], x.shape[1], _ptr(routing.slots), routing.top_k,
+                                    _ptr(routing.offsets), routing.groups, _DTYPES[x.dtype], _ptr(out),
+                                    _stream(stream)), "sharq_permute_rows")
+    return out
+
+
+def combine(y: torch.Tensor, routing: Routing, weights: torch.Tensor | None = None,
+            residual: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Grouped rows y [rows, k] back to their tokens: [m_tok, k] with row t =
+    residual[t] + sum_j weights[t, j] y[slots[t, j]] (weights fp32 [m_tok,
+    top_k], None: 1). out may be residual itself."""
+    _matrix(y, "y")
+    _routing(routing)
+    m_tok, k = routing.m_tok, y.shape[1]
+    _no_grad_inputs(y, weights, residual)
+    if weights is not None:
+        _matrix(weights, "weights", torch.float32, (m_tok, routing.top_k))
+    if residual is not None:
+        _matrix(residual, "residual", y.dtype, (m_tok, k))
+    if out is None:
+        out = _empty((m_tok, k), y.dtype, y.device, stream)
+    _matrix(out, "out", y.dtype, (m_tok, k))
+    _check(lib().sharq_combine(_ptr(y), y.shape[0], m_tok, k, _ptr(routing.slots), _ptr(weights), routing.top_k,
+                               _ptr(residual), _DTYPES[y.dtype], _ptr(out), _stream(stream)), "sharq_combine")
+    return out
+
+
+def combine_backward(dout: torch.Tensor, y: torch.Tensor, routing: Routing, weights: torch.Tensor, stream=None):
+    """Gradients of combine: (dy, dweights) from dout [m_tok, k], the grouped
+    rows y and the weights. dy [rows, k] is zero behind the last group;
+    dweights is fp32 [m_tok, top_k], 0 where an entry has no group. The
+    residual's gradient is dout."""
+    _matrix(y, "y")
+    _routing(routing)
+    m_tok, k = routing.m_tok, y.shape[1]
+    _matrix(dout, "dout", y.dtype, (m_tok, k))
+    _matrix(weights, "weights", torch.float32, (m_tok, routing.top_k))
+    _no_grad_inputs(dout, y, weights)
+    dy = _empty(tuple(y.shape), y.dtype, y.device, stream)
+    dweights = _empty((m_tok, routing.top_k), torch.float32, y.device, stream)
+    _check(lib().sharq_combine_backward(_ptr(dout), _ptr(y), y.shape[0], m_tok, k, _ptr(routing.slots), _ptr(weights),
+                                        routing.top_k, _ptr(routing.offsets), routing.groups, _DTYPES[y.dtype],
+                                        _ptr(dy), _ptr(dweights), _stream(stream)), "sharq_combine_backward")
+    return dy, dweights
+
+
+def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, routing: Routing, scales: torch.Tensor | None = None,
+         base: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Low-rank adapters of many requests beside a shared projection: row r of
+    the result is base[r] + scales[g] * (x[r] a[g]^T) b[g]^T with g the row's
+    adapter, and base[r] (0 without base) for rows that have none.
+      x [m_tok, k], a [adapters, rank, k], b [adapters, n_out, rank] (fp16 or
+      bf16; k, n_out and rank multiples of 8, rank <= 128); routing: route of
+      the rows' adapters ([m_tok] or [m_tok, 1]); scales fp32 [adapters].
+    base is the shared projection's output, e.g. linear()'s; out may be base
+    itself, and x, base and out may be column slices (rows strided)."""
+    _matrix(x, "x", strided=True)
+    _require(x.dtype != torch.float32, "x must be an fp16 or bf16 matrix")
+    for t, name in ((a, "a"), (b, "b")):
+        _require(isinstance(t, torch.Tensor) and t.dim() == 3 and t.dtype == x.dtype and t.is_contiguous(),
+                 f"{name} must be a contiguous tensor of x's type with 3 dimensions")
+        _cuda_here(t, name)
+    m_tok, k = x.shape
+    groups, n_out, rank = b.shape
+    _require(tuple(a.shape) == (groups, rank, k), f"a must have the shape {(groups, rank, k)}")
+    _require(k % 8 == 0 and n_out % 8 == 0 and rank % 8 == 0 and 8 <= rank <= RANK_MAX and k > 0 and n_out > 0,
+             f"k, n_out and rank must be multiples of 8, rank at most {RANK_MAX}")
+    _routing(routing, m_tok)
+    _require(routing.top_k == 1 and routing.groups == groups, "routing must give each row one of the adapters")
+    if scales is not None:
+        _vector(scales, "scales", torch.float32, groups)
+    if base is not None:
+        _matrix(base, "base", x.dtype, (m_tok, n_out), strided=True)
+    _no_grad_inputs(x, a, b, scales, base)
+    if out is None:
+        out = _empty((m_tok, n_out), x.dtype, x.device, stream)
+    _matrix(out, "out", x.dtype, (m_tok, n_out), strided=True)
+    lds = [_ld(t) if t is not None else 0 for t in (x, base, out)]
+    _require(all(v % 8 == 0 for v in lds) and all(t is None or t.data_ptr() % 16 == 0 for t in (x, a, b, base, out)),
+             "x, a, b, base and out must be 16-byte aligned, with row strides that are multiples of 8")
+    _check(lib().sharq_lora(_ptr(x), lds[0], m_tok, k, _ptr(a), _ptr(b), n_out, rank, groups, _ptr(scales),
+                            _ptr(routing.offsets), _ptr(routing.rows), _ptr(routing.slots), _DTYPES[x.dtype],
+                            _ptr(base), lds[1], _ptr(out), lds[2], _stream(stream)), "sharq_lora")
     return out
 
 

@@ -13,12 +13,13 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsharq.so")
-SOURCES = ["api.cu", "prep.cu", "wquant.cu", "gemm.cu", "group.cu"]
-HEADERS = ["layout.h", "sharq_dev.cuh", "sq_internal.h", os.path.join("..", "..", "include", "sharq.h")]
+SOURCES = ["api.cu", "prep.cu", "wquant.cu", "gemm.cu", "group.cu", "norm.cu", "route.cu",
+           "lora.cu"]
+HEADERS = ["layout.h", "sharq_dev.cuh", "vec.cuh", "sq_internal.h", os.path.join("..", "..", "include", "sharq.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-lineinfo", "-O3", "-std=c++17", "-fmad=false",
+    "-lineinfo", "-O3", "-std=c++17", "-fmad=false", "--threads", "0",
     "-Xcompiler", "-fPIC", "-shared",
     "-Xcompiler", "-Werror=return-type", "--diag-error=940",  # a missing return is an error
     "-cudart", "shared",

@@ -1,6 +1,6 @@
 // C ABI of the SharQ library: argument validation, buffer layout, the device
 // status word and the canonical exports. All compute runs in the kernels of
-// prep.cu, wquant.cu and gemm.cu.
+// the other .cu files.
 #include <cuda_runtime.h>
 #include <stdlib.h>
 #include <string.h>
@@ -560,6 +560,230 @@ sharq_status sharq_linear_grouped(const sharq_prep *prep, const int32_t *offsets
     if (st != SHARQ_OK) return st;
     const int64_t gstride = (int64_t)sharq_weight_bytes(wq->n_out, wq->k, wq->fmt);
     st = sq::launch_linear_grouped(ctx, *prep, *wq, offsets_dev, (int32_t)n_groups, rows, gstride, out_dev);
+    g_last_launches = ctx.launches;
+    return st;
+}
+
+// ---------------------------------------------------------------------------
+// Operators in 16 or 32 bits
+
+static bool dtype_ok(int d) { return d == SHARQ_F16 || d == SHARQ_BF16 || d == SHARQ_F32; }
+static int64_t dtype_bytes(int d) { return d == SHARQ_F32 ? 4 : 2; }
+static bool rows_ok(int64_t m) { return m >= 0 && m <= (1ll << 30); }
+static bool width_ok(int64_t k) { return k >= 1 && k <= SHARQ_K_MAX; }
+
+// Whether two byte ranges share a byte (NULL shares none).
+static bool overlap(const void *p, int64_t pb, const void *q, int64_t qb) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a && b && pb > 0 && qb > 0 && a < b + (uintptr_t)qb && b < a + (uintptr_t)pb;
+}
+
+// The same for matrices of m rows with row strides, in bytes; column slices
+// of one buffer (equal strides) share nothing if their columns are disjoint.
+static bool overlap_rows(const void *p, int64_t pld, int64_t pw, const void *q, int64_t qld, int64_t qw, int64_t m) {
+    if (m <= 0 || !overlap(p, (m - 1) * pld + pw, q, (m - 1) * qld + qw)) return false;
+    if (pld != qld) return true;
+    const int64_t diff = (int64_t)(reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p));
+    const int64_t at = ((diff % pld) + pld) % pld;  // q's first column within p's rows
+    return !(at >= pw && at + qw <= pld);
+}
+
+sharq_status sharq_layer_norm(const void *x_dev, int64_t m_tok, int64_t k, const void *ln_w_dev, const void *ln_b_dev,
+                              float eps, int norm, int dtype, void *y_dev, float *mean_dev, float *rstd_dev,
+                              void *stream) {
+    g_last_launches = 0;
+    if (!dtype_ok(dtype) || !rows_ok(m_tok) || !width_ok(k)) return SHARQ_ERR_INVALID_ARG;
+    if ((norm != 0 && norm != 1) || (norm == 1 && (ln_b_dev || mean_dev))) return SHARQ_ERR_INVALID_ARG;
+    if (!(eps > 0.0f) || eps > 3.0e38f) return SHARQ_ERR_INVALID_ARG;
+    if (m_tok == 0) return SHARQ_OK;
+    const int64_t e = dtype_bytes(dtype), bytes = m_tok * k * e;
+    if (!x_dev || !y_dev || !aligned(x_dev, e) || !aligned(y_dev, e) || (ln_w_dev && !aligned(ln_w_dev, e)) ||
+        (ln_b_dev && !aligned(ln_b_dev, e)) || (mean_dev && !aligned(mean_dev, 4)) || (rstd_dev && !aligned(rstd_dev, 4)))
+        return SHARQ_ERR_INVALID_ARG;
+    if (overlap(y_dev, bytes, x_dev, bytes) || overlap(y_dev, bytes, ln_w_dev, k * e) ||
+        overlap(y_dev, bytes, ln_b_dev, k * e))
+        return SHARQ_ERR_INVALID_ARG;
+    const bool vec16 = (k * e) % 16 == 0 && aligned(x_dev, 16) && aligned(y_dev, 16) &&
+                       (!ln_w_dev || aligned(ln_w_dev, 16)) && (!ln_b_dev || aligned(ln_b_dev, 16));
+    sq::LaunchCtx ctx;
+    sharq_status st = make_ctx(stream, ctx);
+    if (st != SHARQ_OK) return st;
+    st = sq::launch_layer_norm(ctx, x_dev, m_tok, k, ln_w_dev, ln_b_dev, eps, norm, dtype, y_dev, mean_dev, rstd_dev,
+                               vec16);
+    g_last_launches = ctx.launches;
+    return st;
+}
+
+size_t sharq_layer_norm_backward_bytes(int64_t m_tok, int64_t k) {
+    if (!rows_ok(m_tok) || !width_ok(k)) return 0;
+    const int64_t b = sq::norm_bwd_parts(m_tok, k) * 2 * k * (int64_t)sizeof(float);
+    return (size_t)sq::round_up(b > 0 ? b : 1, sq::kAlign);
+}
+
+sharq_status sharq_layer_norm_backward(const void *dy_dev, const void *x_dev, int64_t m_tok, int64_t k,
+                                       const void *ln_w_dev, const float *mean_dev, const float *rstd_dev, int norm,
+                                       int dtype, void *dx_dev, float *dw_dev, float *db_dev, void *ws_dev,
+                                       size_t ws_bytes, void *stream) {
+    g_last_launches = 0;
+    if (!dtype_ok(dtype) || !rows_ok(m_tok) || !width_ok(k)) return SHARQ_ERR_INVALID_ARG;
+    if ((norm != 0 && norm != 1) || (norm == 1 && mean_dev)) return SHARQ_ERR_INVALID_ARG;
+    const int64_t e = dtype_bytes(dtype), bytes = m_tok * k * e;
+    if (m_tok > 0) {
+        if (!dy_dev || !x_dev || !dx_dev || !rstd_dev || (norm == 0 && !mean_dev)) return SHARQ_ERR_INVALID_ARG;
+        if (!aligned(dy_dev, e) || !aligned(x_dev, e) || !aligned(dx_dev, e) || !aligned(rstd_dev, 4) ||
+            (mean_dev && !aligned(mean_dev, 4)) || (ln_w_dev && !aligned(ln_w_dev, e)))
+            return SHARQ_ERR_INVALID_ARG;
+        if ((dx_dev != dy_dev && overlap(dx_dev, bytes, dy_dev, bytes)) || overlap(dx_dev, bytes, x_dev, bytes) ||
+            overlap(dx_dev, bytes, ln_w_dev, k * e))
+            return SHARQ_ERR_INVALID_ARG;
+    }
+    if ((dw_dev && !aligned(dw_dev, 4)) || (db_dev && !aligned(db_dev, 4))) return SHARQ_ERR_INVALID_ARG;
+    if (dw_dev || db_dev) {
+        if (overlap(dw_dev, 4 * k, db_dev, 4 * k)) return SHARQ_ERR_INVALID_ARG;
+        if (m_tok > 0 && (!ws_dev || !aligned(ws_dev, sq::kAlign) || ws_bytes < sharq_layer_norm_backward_bytes(m_tok, k)))
+            return SHARQ_ERR_INVALID_ARG;
+    }
+    const bool vec16 = (k * e) % 16 == 0 && aligned(dy_dev, 16) && aligned(x_dev, 16) && aligned(dx_dev, 16) &&
+                       (!ln_w_dev || aligned(ln_w_dev, 16));
+    sq::LaunchCtx ctx;
+    sharq_status st = make_ctx(stream, ctx);
+    if (st != SHARQ_OK) return st;
+    st = sq::launch_layer_norm_backward(ctx, dy_dev, x_dev, m_tok, k, ln_w_dev, mean_dev, rstd_dev, norm, dtype, dx_dev,
+                                        dw_dev, db_dev, static_cast<float *>(ws_dev), vec16);
+    g_last_launches = ctx.launches;
+    return st;
+}
+
+// Sizes of a routing: tokens, choices, groups.
+static bool routing_ok(int64_t m_tok, int64_t top_k, int64_t n_groups) {
+    return rows_ok(m_tok) && top_k >= 1 && top_k <= SHARQ_TOP_K_MAX && m_tok * top_k <= (1ll << 30) && n_groups >= 1 &&
+           n_groups <= SHARQ_GROUPS_MAX;
+}
+
+sharq_status sharq_route(const void *ids_dev, int id_bytes, int64_t m_tok, int64_t top_k, int64_t n_groups,
+                         int32_t *offsets_dev, int32_t *rows_dev, int32_t *slots_dev, void *stream) {
+    g_last_launches = 0;
+    if ((id_bytes != 4 && id_bytes != 8) || !routing_ok(m_tok, top_k, n_groups)) return SHARQ_ERR_INVALID_ARG;
+    if (!offsets_dev || !aligned(offsets_dev, 4)) return SHARQ_ERR_INVALID_ARG;
+    const int64_t n = m_tok * top_k;
+    if (n > 0) {
+        if (!ids_dev || !rows_dev || !slots_dev || !aligned(ids_dev, id_bytes) || !aligned(rows_dev, 4) ||
+            !aligned(slots_dev, 4))
+            return SHARQ_ERR_INVALID_ARG;
+        const int64_t ob = 4 * (n_groups + 1);
+        if (overlap(rows_dev, 4 * n, ids_dev, n * id_bytes) || overlap(slots_dev, 4 * n, ids_dev, n * id_bytes) ||
+            overlap(offsets_dev, ob, ids_dev, n * id_bytes) || overlap(rows_dev, 4 * n, slots_dev, 4 * n) ||
+            overlap(offsets_dev, ob, rows_dev, 4 * n) || overlap(offsets_dev, ob, slots_dev, 4 * n))
+            return SHARQ_ERR_INVALID_ARG;
+    }
+    sq::LaunchCtx ctx;
+    sharq_status st = make_ctx(stream, ctx);
+    if (st != SHARQ_OK) return st;
+    st = sq::launch_route(ctx, ids_dev, id_bytes, m_tok, top_k, n_groups, offsets_dev, rows_dev, slots_dev);
+    g_last_launches = ctx.launches;
+    return st;
+}
+
+sharq_status sharq_permute_rows(const void *x_dev, int64_t m_tok, int64_t k, const int32_t *slots_dev, int64_t top_k,
+                                const int32_t *offsets_dev, int64_t n_groups, int dtype, void *out_dev, void *stream) {
+    g_last_launches = 0;
+    if (!dtype_ok(dtype) || !routing_ok(m_tok, top_k, n_groups) || !width_ok(k)) return SHARQ_ERR_INVALID_ARG;
+    if (m_tok == 0) return SHARQ_OK;
+    const int64_t e = dtype_bytes(dtype);
+    if (!x_dev || !out_dev || !slots_dev || !offsets_dev || !aligned(x_dev, e) || !aligned(out_dev, e) ||
+        !aligned(slots_dev, 4) || !aligned(offsets_dev, 4) || overlap(x_dev, m_tok * k * e, out_dev, m_tok * top_k * k * e))
+        return SHARQ_ERR_INVALID_ARG;
+    const bool vec16 = (k * e) % 16 == 0 && aligned(x_dev, 16) && aligned(out_dev, 16);
+    sq::LaunchCtx ctx;
+    sharq_status st = make_ctx(stream, ctx);
+    if (st != SHARQ_OK) return st;
+    st = sq::launch_permute(ctx, x_dev, m_tok, k, slots_dev, top_k, offsets_dev, n_groups, dtype, out_dev, vec16);
+    g_last_launches = ctx.launches;
+    return st;
+}
+
+sharq_status sharq_combine(const void *y_dev, int64_t rows, int64_t m_tok, int64_t k, const int32_t *slots_dev,
+                           const float *weights_dev, int64_t top_k, const void *residual_dev, int dtype, void *out_dev,
+                           void *stream) {
+    g_last_launches = 0;
+    if (!dtype_ok(dtype) || !routing_ok(m_tok, top_k, 1) || !rows_ok(rows) || !width_ok(k)) return SHARQ_ERR_INVALID_ARG;
+    if (m_tok == 0) return SHARQ_OK;
+    const int64_t e = dtype_bytes(dtype), bytes = m_tok * k * e;
+    if ((rows > 0 && !y_dev) || !out_dev || !slots_dev || !aligned(y_dev, e) || !aligned(out_dev, e) ||
+        !aligned(slots_dev, 4) || (weights_dev && !aligned(weights_dev, 4)) || (residual_dev && !aligned(residual_dev, e)))
+        return SHARQ_ERR_INVALID_ARG;
+    if (overlap(out_dev, bytes, y_dev, rows * k * e) ||
+        (out_dev != residual_dev && overlap(out_dev, bytes, residual_dev, bytes)))
+        return SHARQ_ERR_INVALID_ARG;
+    const bool vec16 = (k * e) % 16 == 0 && aligned(y_dev, 16) && aligned(out_dev, 16) &&
+                       (!residual_dev || aligned(residual_dev, 16));
+    sq::LaunchCtx ctx;
+    sharq_status st = make_ctx(stream, ctx);
+    if (st != SHARQ_OK) return st;
+    st = sq::launch_combine(ctx, y_dev, rows, m_tok, k, slots_dev, weights_dev, top_k, residual_dev, dtype, out_dev, vec16);
+    g_last_launches = ctx.launches;
+    return st;
+}
+
+sharq_status sharq_combine_backward(const void *dout_dev, const void *y_dev, int64_t rows, int64_t m_tok, int64_t k,
+                                    const int32_t *slots_dev, const float *weights_dev, int64_t top_k,
+                                    const int32_t *offsets_dev, int64_t n_groups, int dtype, void *dy_dev,
+                                    float *dweights_dev, void *stream) {
+    g_last_launches = 0;
+    if (!dtype_ok(dtype) || !routing_ok(m_tok, top_k, n_groups) || !rows_ok(rows) || !width_ok(k))
+        return SHARQ_ERR_INVALID_ARG;
+    if (m_tok == 0 && rows == 0) return SHARQ_OK;
+    const int64_t e = dtype_bytes(dtype), bytes = m_tok * k * e, gbytes = rows * k * e;
+    if (!offsets_dev || !aligned(offsets_dev, 4)) return SHARQ_ERR_INVALID_ARG;
+    if (m_tok > 0 && (!dout_dev || !slots_dev || !weights_dev || !dweights_dev)) return SHARQ_ERR_INVALID_ARG;
+    if (rows > 0 && (!dy_dev || !y_dev)) return SHARQ_ERR_INVALID_ARG;
+    if (!aligned(dout_dev, e) || !aligned(y_dev, e) || !aligned(dy_dev, e) || !aligned(slots_dev, 4) ||
+        !aligned(weights_dev, 4) || !aligned(dweights_dev, 4))
+        return SHARQ_ERR_INVALID_ARG;
+    if (overlap(dy_dev, gbytes, y_dev, gbytes) || overlap(dy_dev, gbytes, dout_dev, bytes) ||
+        overlap(dweights_dev, 4 * m_tok * top_k, weights_dev, 4 * m_tok * top_k))
+        return SHARQ_ERR_INVALID_ARG;
+    const bool vec16 = (k * e) % 16 == 0 && aligned(dout_dev, 16) && aligned(y_dev, 16) && aligned(dy_dev, 16);
+    sq::LaunchCtx ctx;
+    sharq_status st = make_ctx(stream, ctx);
+    if (st != SHARQ_OK) return st;
+    st = sq::launch_combine_backward(ctx, dout_dev, y_dev, rows, m_tok, k, slots_dev, weights_dev, top_k, offsets_dev,
+                                     n_groups, dtype, dy_dev, dweights_dev, vec16);
+    g_last_launches = ctx.launches;
+    return st;
+}
+
+sharq_status sharq_lora(const void *x_dev, int64_t ldx, int64_t m_tok, int64_t k, const void *a_dev, const void *b_dev,
+                        int64_t n_out, int64_t rank, int64_t n_groups, const float *scales_dev,
+                        const int32_t *offsets_dev, const int32_t *rows_dev, const int32_t *slots_dev, int dtype,
+                        const void *base_dev, int64_t ldbase, void *out_dev, int64_t ldo, void *stream) {
+    g_last_launches = 0;
+    if (!dtype_ok(dtype) || !routing_ok(m_tok, 1, n_groups) || !width_ok(k)) return SHARQ_ERR_INVALID_ARG;
+    if (n_out < 1 || n_out > (1ll << 20) || rank < 1 || rank > SHARQ_RANK_MAX) return SHARQ_ERR_INVALID_ARG;
+    if (dtype == SHARQ_F32) return SHARQ_ERR_UNSUPPORTED;
+    if (k % 8 || n_out % 8 || rank % 8) return SHARQ_ERR_INVALID_ARG;
+    if (m_tok == 0) return SHARQ_OK;
+    if (!x_dev || !a_dev || !b_dev || !offsets_dev || !rows_dev || !slots_dev || !out_dev) return SHARQ_ERR_INVALID_ARG;
+    const int64_t ld_max = 1ll << 24;
+    if (ldx < k || ldx % 8 || ldx > ld_max || ldo < n_out || ldo % 8 || ldo > ld_max ||
+        (base_dev && (ldbase < n_out || ldbase % 8 || ldbase > ld_max)))
+        return SHARQ_ERR_INVALID_ARG;
+    if (!aligned(x_dev, 16) || !aligned(a_dev, 16) || !aligned(b_dev, 16) || !aligned(out_dev, 16) ||
+        !aligned(base_dev, 16) || !aligned(offsets_dev, 4) || !aligned(rows_dev, 4) || !aligned(slots_dev, 4) ||
+        !aligned(scales_dev, 4))
+        return SHARQ_ERR_INVALID_ARG;
+    if (base_dev == out_dev && ldbase != ldo) return SHARQ_ERR_INVALID_ARG;
+    const int64_t span = ((m_tok - 1) * ldo + n_out) * 2;
+    if (overlap_rows(out_dev, 2 * ldo, 2 * n_out, x_dev, 2 * ldx, 2 * k, m_tok) ||
+        (base_dev && base_dev != out_dev &&
+         overlap_rows(out_dev, 2 * ldo, 2 * n_out, base_dev, 2 * ldbase, 2 * n_out, m_tok)) ||
+        overlap(out_dev, span, a_dev, n_groups * rank * k * 2) || overlap(out_dev, span, b_dev, n_groups * rank * n_out * 2))
+        return SHARQ_ERR_INVALID_ARG;
+    sq::LaunchCtx ctx;
+    sharq_status st = make_ctx(stream, ctx);
+    if (st != SHARQ_OK) return st;
+    st = sq::launch_lora(ctx, x_dev, ldx, m_tok, k, a_dev, b_dev, n_out, rank, n_groups, scales_dev, offsets_dev, rows_dev,
+                         slots_dev, dtype, base_dev, ldbase, out_dev, ldo);
     g_last_launches = ctx.launches;
     return st;
 }

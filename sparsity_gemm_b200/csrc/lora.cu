@@ -1,0 +1,400 @@
+// Low-rank adapters of many requests beside a shared projection.
+//
+//   out[row] = base[row] + scale[g] * (x[row] A[g]^T) B[g]^T,  g the row's group
+//
+// with A [groups][rank][k] and B [groups][n][rank]; rows come sorted by group
+// (offsets, rows: the output of sharq_route), rows without a group keep base.
+//
+// One launch does both products. A cluster takes a tile of rows of one group:
+// its CTAs split k for h = x A^T, add their parts through distributed shared
+// memory, and then split the columns for out = base + scale h B^T. So x, base
+// and out cross HBM once, h never leaves the SMs, and A and B are read once
+// per tile (from L2 after the first).
+//
+// Both products are memory-bound (2 rank operations per 2-byte element of x),
+// so the operands go from global memory straight into the registers of
+// m16n8k16 tensor-core instructions. A dot product may take its terms in any
+// order as long as both operands agree, so a lane loads 8 consecutive
+// elements (16 bytes) of its row and uses them where the instruction expects
+// elements 2q, 2q+1, 2q+8, 2q+9 of two steps; the columns of the second
+// product are permuted the same way, so that a lane's results are 8
+// consecutive columns.
+//
+// h is binary32. For the second product each row is scaled by a power of two
+// and split into two 16-bit terms (the rounded value and the rounded rest),
+// which keeps 2^-16 (bf16) or 2^-22 (fp16) of the row's largest value instead
+// of 2^-8 or 2^-11: the only rounding that shows is the output's own.
+#include <cuda_runtime.h>
+
+#include "sharq_dev.cuh"
+#include "sq_internal.h"
+#include "vec.cuh"
+
+namespace sq {
+
+constexpr int kLoraThreads = 256;
+constexpr int kLoraWarps = kLoraThreads / 32;
+
+struct LoraParams {
+    const void *x, *a, *b, *base;
+    const float *scales;
+    void *out;
+    const int32_t *offsets, *rows, *slots;
+    int64_t ldx, ldbase, ldo;
+    int64_t m;
+    int32_t k, n, rank, groups;
+    int32_t nsplit;  // clusters that share a tile, each with its part of the columns
+    unsigned *status;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, __half) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, __nv_bfloat16) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) { return __uint_as_float(ld_cluster_u32(addr)); }
+
+// The tile's group and rows, found by warp 0 in the offsets (in shared
+// memory). tile_s: [0] group (-1: no such tile, -2: bad offsets), [1] first
+// grouped row, [2] rows.
+__device__ __forceinline__ void find_tile(const int32_t *off, int groups, int64_t m, int tile_rows, int tile,
+                                          int32_t *tile_s) {
+    const int lane = threadIdx.x & 31;
+    bool ok = off[0] == 0 && off[groups] <= m;
+    int32_t carry = 0, group = -1, first = 0;
+    for (int base = 0; base < groups; base += 32) {
+        const int g = base + lane;
+        int32_t t = 0, a = 0;
+        if (g < groups) {
+            a = off[g];
+            const int32_t b = off[g + 1];
+            if (b < a || a < 0 || b > m) ok = false;
+            else t = (b - a + tile_rows - 1) / tile_rows;
+        }
+        int32_t inc = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        const int32_t at = tile - (carry + inc - t);  // the tile's place in my group
+        const bool here = at >= 0 && at < t;
+        const unsigned who = __ballot_sync(0xFFFFFFFFu, here);
+        if (who) {
+            const int src = __ffs((int)who) - 1;
+            group = base + src;
+            first = __shfl_sync(0xFFFFFFFFu, a + at * tile_rows, src);
+        }
+        carry += __shfl_sync(0xFFFFFFFFu, inc, 31);
+    }
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (lane == 0) {
+        tile_s[0] = ok ? group : -2;
+        tile_s[1] = first;
+        tile_s[2] = ok && group >= 0 ? min(tile_rows, off[group + 1] - first) : 0;
+    }
+}
+
+// MT: 16-row blocks of a tile. NB: 8-column blocks of the padded rank.
+template <typename T, int MT, int NB>
+struct LoraCfg {
+    static constexpr int kRows = 16 * MT, kRank = 8 * NB;
+    static constexpr int kLd = kRank + 8;   // row stride of the binary32 parts and of the 16-bit terms
+    static constexpr int kSmem = kLoraWarps * kRows * kLd * 4 + 2 * kRows * kLd * 2;
+    static constexpr int kStep = NB >= 8 ? 1 : 2;  // steps of 32 elements of k in flight
+};
+
+template <typename T, int MT, int NB>
+__global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraParams p) {
+    using C = LoraCfg<T, MT, NB>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    float *part = reinterpret_cast<float *>(smem);  // [warps][rows][kLd]; [0]: the CTA's sum
+    uint16_t *hh = reinterpret_cast<uint16_t *>(smem + kLoraWarps * C::kRows * C::kLd * 4);  // [rows][kLd]
+    uint16_t *hl = hh + C::kRows * C::kLd;
+    __shared__ int32_t off[kGroupsMax + 1];
+    __shared__ int32_t tile_s[3];
+    __shared__ int32_t row_s[C::kRows];
+    __shared__ float scale_s[C::kRows];
+    griddep_wait();
+    griddep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
+    uint32_t csize;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
+    const uint32_t crank = cluster_ctarank();
+    const int cluster_id = (int)(blockIdx.x / csize);
+    const int tile = cluster_id / p.nsplit, part_n = cluster_id % p.nsplit;
+
+    for (int i = threadIdx.x; i <= p.groups; i += kLoraThreads) off[i] = p.offsets[i];
+    __syncthreads();
+    if (warp == 0) find_tile(off, p.groups, p.m, C::kRows, tile, tile_s);
+    __syncthreads();
+    const int group = tile_s[0], first = tile_s[1], count = tile_s[2];
+    if (group == -2) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, kSiteBadOffsets);
+        return;
+    }
+    if (group >= 0) {
+        if (threadIdx.x < C::kRows) {
+            int32_t r = -1;
+            if ((int)threadIdx.x < count) {
+                r = p.rows[first + threadIdx.x];
+                if (r < 0 || r >= p.m) {
+                    record_status(p.status, kSiteBadRowIndex);
+                    r = -1;
+                }
+            }
+            row_s[threadIdx.x] = r;
+        }
+        __syncthreads();
+
+        // h = x A^T over this CTA's steps of k; warps take turns
+        const T *a = static_cast<const T *>(p.a) + (int64_t)group * p.rank * p.k;
+        const T *xr[MT][2];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int32_t r = row_s[16 * i + 8 * h + g8];
+                xr[i][h] = r >= 0 ? static_cast<const T *>(p.x) + (int64_t)r * p.ldx : nullptr;
+            }
+        float acc[MT][NB][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
+        const int steps = (p.k + 32 * C::kStep - 1) / (32 * C::kStep);
+        const int s0 = (int)((int64_t)steps * crank / csize), s1 = (int)((int64_t)steps * (crank + 1) / csize);
+        for (int s = s0 + warp; s < s1; s += kLoraWarps) {
+            uint4 xv[C::kStep][MT][2], av[C::kStep][NB];
+#pragma unroll
+            for (int u = 0; u < C::kStep; ++u) {
+                const int kk = (s * C::kStep + u) * 32 + q * 8;
+                const bool in = kk < p.k;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const int r = 8 * j + g8;
+                    av[u][j] = in && r < p.rank ? __ldg(reinterpret_cast<const uint4 *>(a + (int64_t)r * p.k + kk))
+                                                : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        xv[u][i][h] = in && xr[i][h] ? __ldg(reinterpret_cast<const uint4 *>(xr[i][h] + kk))
+                                                     : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < C::kStep; ++u)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        const uint4 &x0 = xv[u][i][0], &x1 = xv[u][i][1], &b = av[u][j];
+                        mma16816(acc[i][j], x0.x, x1.x, x0.y, x1.y, b.x, b.y, T());
+                        mma16816(acc[i][j], x0.z, x1.z, x0.w, x1.w, b.z, b.w, T());
+                    }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                float *d = part + (warp * C::kRows + 16 * i + g8) * C::kLd + 8 * j + 2 * q;
+                *reinterpret_cast<float2 *>(d) = make_float2(acc[i][j][0], acc[i][j][1]);
+                *reinterpret_cast<float2 *>(d + 8 * C::kLd) = make_float2(acc[i][j][2], acc[i][j][3]);
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < C::kRows * C::kRank; i += kLoraThreads) {
+            float *d = part + (i / C::kRank) * C::kLd + i % C::kRank;
+            float sum = d[0];
+#pragma unroll
+            for (int w = 1; w < kLoraWarps; ++w) sum += d[w * C::kRows * C::kLd];
+            d[0] = sum;
+        }
+        if (csize > 1) cluster_sync();
+        else __syncthreads();
+        // every CTA adds the parts in rank order, so all hold the same h
+        const float scale = p.scales ? p.scales[group] : 1.0f;
+        for (int r = warp; r < C::kRows; r += kLoraWarps) {
+            constexpr int kPer = (C::kRank + 31) / 32;
+            float h[kPer], top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int c = i * 32 + lane;
+                h[i] = 0.0f;
+                if (c < C::kRank) {
+                    const uint32_t at = smem_u32(part + r * C::kLd + c);
+                    if (csize == 1) h[i] = part[r * C::kLd + c];
+                    else
+                        for (uint32_t z = 0; z < csize; ++z) h[i] += ld_cluster_f32(mapa_shared(at, z));
+                }
+                top = fmaxf(top, fabsf(h[i]));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            // a power of two that brings the row's largest value to [1, 2)
+            int e = (int)(__float_as_uint(top) >> 23) - 127;
+            e = e < -100 ? -100 : e > 126 ? 0 : e;
+            const float down = pow2f(-e), up = pow2f(e);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int c = i * 32 + lane;
+                if (c < C::kRank) {
+                    const float v = h[i] * down;
+                    const T hi = narrow<T>(v);
+                    const T lo = narrow<T>(v - widen(hi));
+                    memcpy(hh + r * C::kLd + c, &hi, 2);
+                    memcpy(hl + r * C::kLd + c, &lo, 2);
+                }
+            }
+            if (lane == 0) scale_s[r] = scale * up;
+        }
+        __syncthreads();
+
+        // out = base + scale h B^T over this CTA's blocks of 32 columns
+        const T *b = static_cast<const T *>(p.b) + (int64_t)group * p.n * p.rank;
+        const T *base = static_cast<const T *>(p.base);
+        T *out = static_cast<T *>(p.out);
+        const int blocks = (p.n + 31) / 32;
+        const int64_t piece = (int64_t)part_n * csize + crank, pieces = (int64_t)p.nsplit * csize;
+        const int c0 = (int)(blocks * piece / pieces), c1 = (int)(blocks * (piece + 1) / pieces);
+        for (int c = c0 + warp; c < c1; c += kLoraWarps) {
+            const int n0 = 32 * c, col = n0 + 8 * q;
+            uint4 bv[4][(NB + 3) / 4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = n0 + 8 * (g8 >> 1) + 2 * j + (g8 & 1);
+                const T *br = b + (int64_t)row * p.rank;
+#pragma unroll
+                for (int s = 0; s < (NB + 3) / 4; ++s) {
+                    bv[j][s] = make_uint4(0, 0, 0, 0);
+                    if (NB == 2) {  // one step of 16
+                        if (row < p.n && 4 * q < p.rank) {
+                            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(br + 4 * q));
+                            bv[j][s].x = v.x;
+                            bv[j][s].y = v.y;
+                        }
+                    } else if (row < p.n && 32 * s + 8 * q < p.rank) {
+                        bv[j][s] = __ldg(reinterpret_cast<const uint4 *>(br + 32 * s + 8 * q));
+                    }
+                }
+            }
+            uint4 old[MT][2];
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int32_t r = row_s[16 * i + 8 * h + g8];
+                    old[i][h] = make_uint4(0, 0, 0, 0);
+                    if (base && r >= 0 && col < p.n)
+                        old[i][h] = *reinterpret_cast<const uint4 *>(base + (int64_t)r * p.ldbase + col);
+                }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                float d[4][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[j][e] = 0.0f;
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const uint16_t *hp = (z ? hl : hh) + (16 * i + g8) * C::kLd;
+#pragma unroll
+                    for (int s = 0; s < (NB + 3) / 4; ++s) {
+                        if (NB == 2) {
+                            const uint2 h0 = *reinterpret_cast<const uint2 *>(hp + 4 * q);
+                            const uint2 h1 = *reinterpret_cast<const uint2 *>(hp + 8 * C::kLd + 4 * q);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) mma16816(d[j], h0.x, h1.x, h0.y, h1.y, bv[j][s].x, bv[j][s].y, T());
+                        } else {
+                            const uint4 h0 = *reinterpret_cast<const uint4 *>(hp + 32 * s + 8 * q);
+                            const uint4 h1 = *reinterpret_cast<const uint4 *>(hp + 8 * C::kLd + 32 * s + 8 * q);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                mma16816(d[j], h0.x, h1.x, h0.y, h1.y, bv[j][s].x, bv[j][s].y, T());
+                                mma16816(d[j], h0.z, h1.z, h0.w, h1.w, bv[j][s].z, bv[j][s].w, T());
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int32_t r = row_s[16 * i + 8 * h + g8];
+                    if (r >= 0 && col < p.n) {
+                        const float sc = scale_s[16 * i + 8 * h + g8];
+                        float f[8];
+                        Vec<T, 8>::unpack(old[i][h], f);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            f[2 * j] = fmaf(sc, d[j][2 * h], f[2 * j]);
+                            f[2 * j + 1] = fmaf(sc, d[j][2 * h + 1], f[2 * j + 1]);
+                        }
+                        *reinterpret_cast<uint4 *>(out + (int64_t)r * p.ldo + col) = Vec<T, 8>::pack(f);
+                    }
+                }
+            }
+        }
+    }
+    // rows without a group: base (or zero), unless they are there already
+    if (p.base != p.out) {
+        const int64_t warps = (int64_t)gridDim.x * kLoraWarps;
+        for (int64_t r = (int64_t)blockIdx.x * kLoraWarps + warp; r < p.m; r += warps) {
+            if (p.slots[r] >= 0) continue;
+            const T *src = static_cast<const T *>(p.base) + r * p.ldbase;
+            T *dst = static_cast<T *>(p.out) + r * p.ldo;
+            for (int c = 8 * lane; c < p.n; c += 256)
+                *reinterpret_cast<uint4 *>(dst + c) =
+                    p.base ? *reinterpret_cast<const uint4 *>(src + c) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    if (group >= 0 && csize > 1) cluster_sync();  // no CTA leaves while another reads its part
+}
+
+template <typename T, int MT, int NB>
+static sharq_status lora_run(LaunchCtx &ctx, LoraParams p) {
+    using C = LoraCfg<T, MT, NB>;
+    if (C::kSmem > 40 * 1024)
+        SQ_CUDA_TRY(cudaFuncSetAttribute(lora_kernel<T, MT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+    const int64_t few = p.groups < p.m ? p.groups : p.m;
+    int64_t tiles = p.m / C::kRows + few;  // bound on sum ceil(rows of a group / kRows)
+    if (tiles > p.m) tiles = p.m;
+    // Split a tile until the CTAs fill the GPU twice, as long as a CTA keeps
+    // a few hundred elements of k and of the columns.
+    int cluster = 1;
+    while (cluster < 8 && tiles * cluster < 2 * ctx.num_sms && p.k >= 512 * cluster) cluster *= 2;
+    p.nsplit = 1;
+    while (p.nsplit < 16 && tiles * cluster * p.nsplit < ctx.num_sms && p.n >= 512 * cluster * p.nsplit) p.nsplit *= 2;
+    return launch_pdl(ctx, lora_kernel<T, MT, NB>, tiles * cluster * p.nsplit, kLoraThreads, C::kSmem, cluster, p);
+}
+
+template <typename T>
+static sharq_status lora_any(LaunchCtx &ctx, const LoraParams &p) {
+    // rows of a group, on average, decide how many a tile holds; the
+    // accumulators of a warp (kRows x rank) decide how many it can hold
+    const bool many = p.m > 16 * (int64_t)p.groups;
+    if (p.rank <= 16) return many ? lora_run<T, 4, 2>(ctx, p) : lora_run<T, 1, 2>(ctx, p);
+    if (p.rank <= 32) return many ? lora_run<T, 4, 4>(ctx, p) : lora_run<T, 1, 4>(ctx, p);
+    if (p.rank <= 64) return many ? lora_run<T, 2, 8>(ctx, p) : lora_run<T, 1, 8>(ctx, p);
+    return lora_run<T, 1, 16>(ctx, p);
+}
+
+sharq_status launch_lora(LaunchCtx &ctx, const void *x, int64_t ldx, int64_t m, int64_t k, const void *a, const void *b,
+                         int64_t n, int64_t rank, int64_t groups, const float *scales, const int32_t *offsets,
+                         const int32_t *rows, const int32_t *slots, int dtype, const void *base, int64_t ldbase, void *out,
+                         int64_t ldo) {
+    if (m == 0) return SHARQ_OK;
+    LoraParams p{x, a, b, base, scales, out, offsets, rows, slots, ldx, ldbase, ldo, m,
+                 (int32_t)k, (int32_t)n, (int32_t)rank, (int32_t)groups, 1, ctx.status};
+    return dtype == SHARQ_F16 ? lora_any<__half>(ctx, p) : lora_any<__nv_bfloat16>(ctx, p);
+}
+
+}  // namespace sq

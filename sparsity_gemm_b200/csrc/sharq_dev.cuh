@@ -375,7 +375,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigne
 // groups before g.
 
 // Device-side argument codes (status word values 0x2xx).
-enum : unsigned { kSiteBadOffsets = 0x201, kSiteBadRowIndex = 0x202 };
+enum : unsigned { kSiteBadOffsets = 0x201, kSiteBadRowIndex = 0x202, kSiteBadSlot = 0x203 };
 
 // Builds tiles[0 .. groups] in shared memory with the calling warp (all 32
 // lanes must call). Returns, in every lane, whether the offsets are valid:

@@ -42,6 +42,31 @@ sharq_status launch_wait_probe(LaunchCtx &ctx, uint64_t limit_ns);
 void note_launches(int n);
 sharq_status launch_div_check(LaunchCtx &ctx, uint64_t count, uint64_t seed, uint64_t *mismatches, float *examples);
 
+// Operators in 16 or 32 bits (norm.cu, route.cu, lora.cu). vec16: rows and
+// buffers allow 16-byte accesses.
+sharq_status launch_layer_norm(LaunchCtx &ctx, const void *x, int64_t rows, int64_t k, const void *w, const void *b,
+                               float eps, int norm, int dtype, void *y, float *mean, float *rstd, bool vec16);
+// Partial rows ([2][k] floats each) of the weight gradients.
+int64_t norm_bwd_parts(int64_t rows, int64_t k);
+sharq_status launch_layer_norm_backward(LaunchCtx &ctx, const void *dy, const void *x, int64_t rows, int64_t k,
+                                        const void *w, const float *mean, const float *rstd, int norm, int dtype,
+                                        void *dx, float *dw, float *db, float *part, bool vec16);
+sharq_status launch_route(LaunchCtx &ctx, const void *ids, int id_bytes, int64_t tokens, int64_t top_k, int64_t groups,
+                          int32_t *offsets, int32_t *rows, int32_t *slots);
+sharq_status launch_permute(LaunchCtx &ctx, const void *x, int64_t tokens, int64_t k, const int32_t *slots, int64_t top_k,
+                            const int32_t *offsets, int64_t groups, int dtype, void *out, bool vec16);
+sharq_status launch_combine(LaunchCtx &ctx, const void *y, int64_t n_rows, int64_t tokens, int64_t k,
+                            const int32_t *slots, const float *weights, int64_t top_k, const void *residual, int dtype,
+                            void *out, bool vec16);
+sharq_status launch_combine_backward(LaunchCtx &ctx, const void *dout, const void *y, int64_t n_rows, int64_t tokens,
+                                     int64_t k, const int32_t *slots, const float *weights, int64_t top_k,
+                                     const int32_t *offsets, int64_t groups, int dtype, void *dy, float *dweights,
+                                     bool vec16);
+sharq_status launch_lora(LaunchCtx &ctx, const void *x, int64_t ldx, int64_t m, int64_t k, const void *a, const void *b,
+                         int64_t n, int64_t rank, int64_t groups, const float *scales, const int32_t *offsets,
+                         const int32_t *rows, const int32_t *slots, int dtype, const void *base, int64_t ldbase, void *out,
+                         int64_t ldo);
+
 }  // namespace sq
 
 #define SQ_CUDA_TRY(expr)                                         \
