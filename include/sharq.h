@@ -641,11 +641,15 @@ sharq_status sharq_combine_backward(const void *dout_dev, const void *y_dev, int
  * x, base or out where their columns are disjoint.
  * Invalid offsets write nothing, invalid rows are skipped; both are reported
  * by sharq_get_last_error as SHARQ_ERR_INVALID_ARG.
+ *   ws_dev    workspace of sharq_lora_bytes(m_tok, rank, n_groups) bytes,
+ *             256-byte aligned; NULL where that is 0 (few rows per adapter).
  */
+size_t sharq_lora_bytes(int64_t m_tok, int64_t rank, int64_t n_groups);
 sharq_status sharq_lora(const void *x_dev, int64_t ldx, int64_t m_tok, int64_t k, const void *a_dev, const void *b_dev,
                         int64_t n_out, int64_t rank, int64_t n_groups, const float *scales_dev,
                         const int32_t *offsets_dev, const int32_t *rows_dev, const int32_t *slots_dev, int dtype,
-                        const void *base_dev, int64_t ldbase, void *out_dev, int64_t ldo, void *stream);
+                        const void *base_dev, int64_t ldbase, void *out_dev, int64_t ldo, void *ws_dev, size_t ws_bytes,
+                        void *stream);
 
 /*
  * Canonical host copies of a prepared activation, for inspection and tests.

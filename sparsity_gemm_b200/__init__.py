@@ -111,7 +111,9 @@ def lib():
         L.sharq_permute_rows.argtypes = [vp, i64, i64, vp, i64, vp, i64, i32, vp, vp]
         L.sharq_combine.argtypes = [vp, i64, i64, i64, vp, vp, i64, vp, i32, vp, vp]
         L.sharq_combine_backward.argtypes = [vp, vp, i64, i64, i64, vp, vp, i64, vp, i64, i32, vp, vp, vp]
-        L.sharq_lora.argtypes = [vp, i64, i64, i64, vp, vp, i64, i64, i64, vp, vp, vp, vp, i32, vp, i64, vp, i64, vp]
+        L.sharq_lora_bytes.argtypes = [i64, i64, i64]
+        L.sharq_lora_bytes.restype = sz
+        L.sharq_lora.argtypes = [vp, i64, i64, i64, vp, vp, i64, i64, i64, vp, vp, vp, vp, i32, vp, i64, vp, i64, vp, sz, vp]
         L.sharq_status_string.argtypes = [i32]
         L.sharq_status_string.restype = C.c_char_p
         L.sharq_last_launch_count.restype = i32
@@ -791,9 +793,12 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, routing: Routing, sc
     lds = [_ld(t) if t is not None else 0 for t in (x, base, out)]
     _require(all(v % 8 == 0 for v in lds) and all(t is None or t.data_ptr() % 16 == 0 for t in (x, a, b, base, out)),
              "x, a, b, base and out must be 16-byte aligned, with row strides that are multiples of 8")
+    nbytes = int(lib().sharq_lora_bytes(m_tok, rank, groups))
+    ws = _empty((nbytes,), torch.uint8, x.device, stream) if nbytes else None
     _check(lib().sharq_lora(_ptr(x), lds[0], m_tok, k, _ptr(a), _ptr(b), n_out, rank, groups, _ptr(scales),
                             _ptr(routing.offsets), _ptr(routing.rows), _ptr(routing.slots), _DTYPES[x.dtype],
-                            _ptr(base), lds[1], _ptr(out), lds[2], _stream(stream)), "sharq_lora")
+                            _ptr(base), lds[1], _ptr(out), lds[2], _ptr(ws), nbytes, _stream(stream)),
+           "sharq_lora")
     return out
 
 

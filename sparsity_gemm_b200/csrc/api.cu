@@ -753,10 +753,16 @@ sharq_status sharq_combine_backward(const void *dout_dev, const void *y_dev, int
     return st;
 }
 
+size_t sharq_lora_bytes(int64_t m_tok, int64_t rank, int64_t n_groups) {
+    if (!routing_ok(m_tok, 1, n_groups) || rank < 1 || rank > SHARQ_RANK_MAX) return 0;
+    return (size_t)sq::lora_ws_bytes(m_tok, rank, n_groups);
+}
+
 sharq_status sharq_lora(const void *x_dev, int64_t ldx, int64_t m_tok, int64_t k, const void *a_dev, const void *b_dev,
                         int64_t n_out, int64_t rank, int64_t n_groups, const float *scales_dev,
                         const int32_t *offsets_dev, const int32_t *rows_dev, const int32_t *slots_dev, int dtype,
-                        const void *base_dev, int64_t ldbase, void *out_dev, int64_t ldo, void *stream) {
+                        const void *base_dev, int64_t ldbase, void *out_dev, int64_t ldo, void *ws_dev, size_t ws_bytes,
+                        void *stream) {
     g_last_launches = 0;
     if (!dtype_ok(dtype) || !routing_ok(m_tok, 1, n_groups) || !width_ok(k)) return SHARQ_ERR_INVALID_ARG;
     if (n_out < 1 || n_out > (1ll << 20) || rank < 1 || rank > SHARQ_RANK_MAX) return SHARQ_ERR_INVALID_ARG;
@@ -773,6 +779,8 @@ sharq_status sharq_lora(const void *x_dev, int64_t ldx, int64_t m_tok, int64_t k
         !aligned(scales_dev, 4))
         return SHARQ_ERR_INVALID_ARG;
     if (base_dev == out_dev && ldbase != ldo) return SHARQ_ERR_INVALID_ARG;
+    const size_t need = sharq_lora_bytes(m_tok, rank, n_groups);
+    if (need && (!ws_dev || !aligned(ws_dev, sq::kAlign) || ws_bytes < need)) return SHARQ_ERR_INVALID_ARG;
     const int64_t span = ((m_tok - 1) * ldo + n_out) * 2;
     if (overlap_rows(out_dev, 2 * ldo, 2 * n_out, x_dev, 2 * ldx, 2 * k, m_tok) ||
         (base_dev && base_dev != out_dev &&
@@ -783,7 +791,7 @@ sharq_status sharq_lora(const void *x_dev, int64_t ldx, int64_t m_tok, int64_t k
     sharq_status st = make_ctx(stream, ctx);
     if (st != SHARQ_OK) return st;
     st = sq::launch_lora(ctx, x_dev, ldx, m_tok, k, a_dev, b_dev, n_out, rank, n_groups, scales_dev, offsets_dev, rows_dev,
-                         slots_dev, dtype, base_dev, ldbase, out_dev, ldo);
+                         slots_dev, dtype, base_dev, ldbase, out_dev, ldo, ws_dev);
     g_last_launches = ctx.launches;
     return st;
 }

@@ -1129,6 +1129,18 @@ static bool make_code_map(CUtensorMap *tm, const void *base, uint64_t row_bytes,
     return r == CUDA_SUCCESS;
 }
 
+bool make_row_map(CUtensorMap *tm, const void *base, uint64_t cols, uint64_t rows, uint64_t ld_bytes, uint32_t box_rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {ld_bytes};
+    cuuint32_t box[2] = {64, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 3-D byte tensor [groups][rows][row_bytes] with `group_stride` bytes
 // between groups; box = kBKBytes x box_rows x 1, swizzled like make_code_map.
 static bool make_grouped_code_map(CUtensorMap *tm, const void *base, uint64_t row_bytes, uint64_t rows,

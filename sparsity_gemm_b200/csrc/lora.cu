@@ -43,8 +43,11 @@ struct LoraParams {
     int64_t ldx, ldbase, ldo;
     int64_t m;
     int32_t k, n, rank, groups;
-    int32_t nsplit;  // clusters that share a tile, each with its part of the columns
+    int32_t nsplit;  // clusters (expand: CTAs) that share a tile, each with its part of the columns
     unsigned *status;
+    uint64_t wait_ns;
+    void *h;         // two-launch form: [grouped row][2][padded rank] 16-bit terms
+    float *hscale;   // and their power of two
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -100,6 +103,112 @@ __device__ __forceinline__ void find_tile(const int32_t *off, int groups, int64_
         tile_s[0] = ok ? group : -2;
         tile_s[1] = first;
         tile_s[2] = ok && group >= 0 ? min(tile_rows, off[group + 1] - first) : 0;
+    }
+}
+
+// out = base + scale h B^T for the tile's rows, over piece `piece` of `pieces`
+// of the blocks of 32 columns; warps take turns. hh, hl: the two terms of h.
+template <typename T, int MT, int NB>
+__device__ __forceinline__ void expand_tile(const LoraParams &p, int group, const int32_t *row_s, const float *scale_s,
+                                            const uint16_t *hh, const uint16_t *hl, int64_t piece, int64_t pieces) {
+    constexpr int kLd = 8 * NB + 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
+            const T *b = static_cast<const T *>(p.b) + (int64_t)group * p.n * p.rank;
+            const T *base = static_cast<const T *>(p.base);
+            T *out = static_cast<T *>(p.out);
+            const int blocks = (p.n + 31) / 32;
+            const int c0 = (int)(blocks * piece / pieces), c1 = (int)(blocks * (piece + 1) / pieces);
+            for (int c = c0 + warp; c < c1; c += kLoraWarps) {
+                const int n0 = 32 * c, col = n0 + 8 * q;
+                uint4 bv[4][(NB + 3) / 4];
+    #pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = n0 + 8 * (g8 >> 1) + 2 * j + (g8 & 1);
+                    const T *br = b + (int64_t)row * p.rank;
+    #pragma unroll
+                    for (int s = 0; s < (NB + 3) / 4; ++s) {
+                        bv[j][s] = make_uint4(0, 0, 0, 0);
+                        if (NB == 2) {  // one step of 16
+                            if (row < p.n && 4 * q < p.rank) {
+                                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(br + 4 * q));
+                                bv[j][s].x = v.x;
+                                bv[j][s].y = v.y;
+                            }
+                        } else if (row < p.n && 32 * s + 8 * q < p.rank) {
+                            bv[j][s] = __ldg(reinterpret_cast<const uint4 *>(br + 32 * s + 8 * q));
+                        }
+                    }
+                }
+                uint4 old[MT][2];
+    #pragma unroll
+                for (int i = 0; i < MT; ++i)
+    #pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int32_t r = row_s[16 * i + 8 * h + g8];
+                        old[i][h] = make_uint4(0, 0, 0, 0);
+                        if (base && r >= 0 && col < p.n)
+                            old[i][h] = *reinterpret_cast<const uint4 *>(base + (int64_t)r * p.ldbase + col);
+                    }
+    #pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    float d[4][4];
+    #pragma unroll
+                    for (int j = 0; j < 4; ++j)
+    #pragma unroll
+                        for (int e = 0; e < 4; ++e) d[j][e] = 0.0f;
+    #pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const uint16_t *hp = (z ? hl : hh) + (16 * i + g8) * kLd;
+    #pragma unroll
+                        for (int s = 0; s < (NB + 3) / 4; ++s) {
+                            if (NB == 2) {
+                                const uint2 h0 = *reinterpret_cast<const uint2 *>(hp + 4 * q);
+                                const uint2 h1 = *reinterpret_cast<const uint2 *>(hp + 8 * kLd + 4 * q);
+    #pragma unroll
+                                for (int j = 0; j < 4; ++j) mma16816(d[j], h0.x, h1.x, h0.y, h1.y, bv[j][s].x, bv[j][s].y, T());
+                            } else {
+                                const uint4 h0 = *reinterpret_cast<const uint4 *>(hp + 32 * s + 8 * q);
+                                const uint4 h1 = *reinterpret_cast<const uint4 *>(hp + 8 * kLd + 32 * s + 8 * q);
+    #pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    mma16816(d[j], h0.x, h1.x, h0.y, h1.y, bv[j][s].x, bv[j][s].y, T());
+                                    mma16816(d[j], h0.z, h1.z, h0.w, h1.w, bv[j][s].z, bv[j][s].w, T());
+                                }
+                            }
+                        }
+                    }
+    #pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int32_t r = row_s[16 * i + 8 * h + g8];
+                        if (r >= 0 && col < p.n) {
+                            const float sc = scale_s[16 * i + 8 * h + g8];
+                            float f[8];
+                            Vec<T, 8>::unpack(old[i][h], f);
+    #pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                f[2 * j] = fmaf(sc, d[j][2 * h], f[2 * j]);
+                                f[2 * j + 1] = fmaf(sc, d[j][2 * h + 1], f[2 * j + 1]);
+                            }
+                            *reinterpret_cast<uint4 *>(out + (int64_t)r * p.ldo + col) = Vec<T, 8>::pack(f);
+                        }
+                    }
+                }
+            }
+}
+
+// Rows without a group: base (or zero), unless they are there already.
+template <typename T>
+__device__ __forceinline__ void copy_bare_rows(const LoraParams &p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (p.base == p.out) return;
+    const int64_t warps = (int64_t)gridDim.x * kLoraWarps;
+    for (int64_t r = (int64_t)blockIdx.x * kLoraWarps + warp; r < p.m; r += warps) {
+        if (p.slots[r] >= 0) continue;
+        const T *src = static_cast<const T *>(p.base) + r * p.ldbase;
+        T *dst = static_cast<T *>(p.out) + r * p.ldo;
+        for (int c = 8 * lane; c < p.n; c += 256)
+            *reinterpret_cast<uint4 *>(dst + c) =
+                p.base ? *reinterpret_cast<const uint4 *>(src + c) : make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -260,113 +369,279 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraParams p) 
         }
         __syncthreads();
 
-        // out = base + scale h B^T over this CTA's blocks of 32 columns
-        const T *b = static_cast<const T *>(p.b) + (int64_t)group * p.n * p.rank;
-        const T *base = static_cast<const T *>(p.base);
-        T *out = static_cast<T *>(p.out);
-        const int blocks = (p.n + 31) / 32;
         const int64_t piece = (int64_t)part_n * csize + crank, pieces = (int64_t)p.nsplit * csize;
-        const int c0 = (int)(blocks * piece / pieces), c1 = (int)(blocks * (piece + 1) / pieces);
-        for (int c = c0 + warp; c < c1; c += kLoraWarps) {
-            const int n0 = 32 * c, col = n0 + 8 * q;
-            uint4 bv[4][(NB + 3) / 4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = n0 + 8 * (g8 >> 1) + 2 * j + (g8 & 1);
-                const T *br = b + (int64_t)row * p.rank;
-#pragma unroll
-                for (int s = 0; s < (NB + 3) / 4; ++s) {
-                    bv[j][s] = make_uint4(0, 0, 0, 0);
-                    if (NB == 2) {  // one step of 16
-                        if (row < p.n && 4 * q < p.rank) {
-                            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(br + 4 * q));
-                            bv[j][s].x = v.x;
-                            bv[j][s].y = v.y;
-                        }
-                    } else if (row < p.n && 32 * s + 8 * q < p.rank) {
-                        bv[j][s] = __ldg(reinterpret_cast<const uint4 *>(br + 32 * s + 8 * q));
-                    }
-                }
-            }
-            uint4 old[MT][2];
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int32_t r = row_s[16 * i + 8 * h + g8];
-                    old[i][h] = make_uint4(0, 0, 0, 0);
-                    if (base && r >= 0 && col < p.n)
-                        old[i][h] = *reinterpret_cast<const uint4 *>(base + (int64_t)r * p.ldbase + col);
-                }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                float d[4][4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) d[j][e] = 0.0f;
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const uint16_t *hp = (z ? hl : hh) + (16 * i + g8) * C::kLd;
-#pragma unroll
-                    for (int s = 0; s < (NB + 3) / 4; ++s) {
-                        if (NB == 2) {
-                            const uint2 h0 = *reinterpret_cast<const uint2 *>(hp + 4 * q);
-                            const uint2 h1 = *reinterpret_cast<const uint2 *>(hp + 8 * C::kLd + 4 * q);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) mma16816(d[j], h0.x, h1.x, h0.y, h1.y, bv[j][s].x, bv[j][s].y, T());
-                        } else {
-                            const uint4 h0 = *reinterpret_cast<const uint4 *>(hp + 32 * s + 8 * q);
-                            const uint4 h1 = *reinterpret_cast<const uint4 *>(hp + 8 * C::kLd + 32 * s + 8 * q);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                mma16816(d[j], h0.x, h1.x, h0.y, h1.y, bv[j][s].x, bv[j][s].y, T());
-                                mma16816(d[j], h0.z, h1.z, h0.w, h1.w, bv[j][s].z, bv[j][s].w, T());
-                            }
-                        }
-                    }
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int32_t r = row_s[16 * i + 8 * h + g8];
-                    if (r >= 0 && col < p.n) {
-                        const float sc = scale_s[16 * i + 8 * h + g8];
-                        float f[8];
-                        Vec<T, 8>::unpack(old[i][h], f);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            f[2 * j] = fmaf(sc, d[j][2 * h], f[2 * j]);
-                            f[2 * j + 1] = fmaf(sc, d[j][2 * h + 1], f[2 * j + 1]);
-                        }
-                        *reinterpret_cast<uint4 *>(out + (int64_t)r * p.ldo + col) = Vec<T, 8>::pack(f);
-                    }
-                }
-            }
-        }
+        expand_tile<T, MT, NB>(p, group, row_s, scale_s, hh, hl, piece, pieces);
     }
-    // rows without a group: base (or zero), unless they are there already
-    if (p.base != p.out) {
-        const int64_t warps = (int64_t)gridDim.x * kLoraWarps;
-        for (int64_t r = (int64_t)blockIdx.x * kLoraWarps + warp; r < p.m; r += warps) {
-            if (p.slots[r] >= 0) continue;
-            const T *src = static_cast<const T *>(p.base) + r * p.ldbase;
-            T *dst = static_cast<T *>(p.out) + r * p.ldo;
-            for (int c = 8 * lane; c < p.n; c += 256)
-                *reinterpret_cast<uint4 *>(dst + c) =
-                    p.base ? *reinterpret_cast<const uint4 *>(src + c) : make_uint4(0, 0, 0, 0);
-        }
-    }
+    copy_bare_rows<T>(p);
     if (group >= 0 && csize > 1) cluster_sync();  // no CTA leaves while another reads its part
+}
+
+// ---------------------------------------------------------------------------
+// Many rows per adapter: two launches, h in the workspace.
+//
+// The first computes h = x A^T on the tensor cores of the fifth generation:
+// 128 rows of a group per tile, gathered from x four rows per copy, A's rows
+// beside them, k in steps of 64 through a ring of shared-memory stages, the
+// accumulator in tensor memory. The CTAs of a cluster split k and add their
+// parts through distributed shared memory; h leaves as its two 16-bit terms.
+// It is bound by reading x. The second is the fused form's second half on
+// tiles of 64 rows, bound by base and out. Two launches keep both streaming
+// all the time; in one, a tile's reads of x and its writes alternate.
+constexpr int kShRows = 128;
+constexpr int kShK = 64;
+constexpr int kShThreads = 192;  // warps 0-3: accumulator; 4: copies; 5: products
+constexpr int kShX = kShRows * kShK * 2;
+
+template <int R>
+struct ShrinkCfg {
+    static constexpr int kStage = kShX + R * kShK * 2;
+    static constexpr int kStages = 100 * 1024 / kStage;  // two CTAs on an SM
+    static constexpr int kLd = R + 4;                    // row stride of the binary32 parts
+    static constexpr int kPart = kShRows * kLd * 4;
+    static constexpr int kSmem = 1024 + (kStages * kStage > kPart ? kStages * kStage : kPart);
+    static constexpr int kTmem = R < 32 ? 32 : R;
+};
+
+// Padded rank of the two-launch form.
+SQ_HD int shrink_rank(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+
+template <typename T, int R>
+__global__ void __launch_bounds__(kShThreads)
+    lora_shrink_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_a, const LoraParams p) {
+    using C = ShrinkCfg<R>;
+    extern __shared__ uint8_t dyn[];
+    __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], done;
+    __shared__ uint32_t tmem_s;
+    __shared__ int32_t off[kGroupsMax + 1];
+    __shared__ int32_t tile_s[3];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
+    float *part = reinterpret_cast<float *>(dyn + (ring - smem_u32(dyn)));
+    griddep_wait();
+    griddep_launch();
+    uint32_t csize;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
+    const uint32_t crank = cluster_ctarank();
+    for (int i = threadIdx.x; i <= p.groups; i += kShThreads) off[i] = p.offsets[i];
+    __syncthreads();
+    if (warp == 0) find_tile(off, p.groups, p.m, kShRows, (int)(blockIdx.x / csize), tile_s);
+    __syncthreads();
+    const int group = tile_s[0], first = tile_s[1], count = tile_s[2];
+    if (group < 0) {  // the same for the whole cluster
+        if (group == -2 && blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, kSiteBadOffsets);
+        return;
+    }
+    if (warp == 5) {
+        tmem_alloc(smem_u32(&tmem_s), C::kTmem);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        mbar_init(smem_u32(&done), 1);
+        mbar_fence_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_s;
+    const int blocks = (p.k + kShK - 1) / kShK;
+    const int b0 = (int)((int64_t)blocks * crank / csize), b1 = (int)((int64_t)blocks * (crank + 1) / csize);
+
+    if (warp == 4) {
+        // Rows past the tile's end are not copied: what their lanes of the
+        // accumulator hold is not read.
+        const int quads = (count + 3) / 4;
+        int32_t r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int32_t v = p.rows[first + min(4 * lane + j, count - 1)];
+            r[j] = v >= 0 && v < p.m ? v : 0;  // reported, and left out, by the second launch
+        }
+        for (int b = b0; b < b1; ++b) {
+            const int i = b - b0, s = i % C::kStages;
+            const bool ok = mbar_wait_own(smem_u32(&empty[s]), ((i / C::kStages) & 1) ^ 1, p.status, kSiteLoraEmpty, p.wait_ns);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            const uint32_t dst = ring + s * C::kStage, bar = smem_u32(&full[s]);
+            if (lane == 0) mbar_arrive_expect_tx(bar, quads * 4 * kShK * 2 + R * kShK * 2);
+            __syncwarp();
+            if (lane < quads) tma_gather4(dst + lane * 4 * kShK * 2, &tm_x, b * kShK, r[0], r[1], r[2], r[3], bar);
+            if (lane == 0) tma_load_2d(dst + kShX, &tm_a, b * kShK, group * p.rank, bar);
+        }
+    } else if (warp == 5) {
+        if (lane == 0) {
+            // D binary32; A and B of type T, both K-major; N = R, M = 128
+            const uint32_t fmt = IsBf16<T>::v ? 1u : 0u;
+            const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(R >> 3) << 17) | ((kShRows >> 4) << 24);
+            for (int b = b0; b < b1; ++b) {
+                const int i = b - b0, s = i % C::kStages;
+                if (!mbar_wait_own(smem_u32(&full[s]), (i / C::kStages) & 1, p.status, kSiteLoraFull, p.wait_ns)) break;
+                tc_fence_after();
+                const uint32_t st = ring + s * C::kStage;
+                const uint64_t dx = smem_desc(st, 16, 8 * kShK * 2, 2u), da = smem_desc(st + kShX, 16, 8 * kShK * 2, 2u);
+#pragma unroll
+                for (int j = 0; j < kShK / 16; ++j) tc_mma_f16(tmem, dx + 2 * j, da + 2 * j, idesc, i != 0 || j != 0);
+                tc_commit(smem_u32(&empty[s]));
+            }
+            tc_commit(smem_u32(&done));
+        }
+        __syncwarp();
+    }
+    // Every thread waits for the products: the ring is free then, and the
+    // parts of h take its place.
+    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_own(smem_u32(&done), 0, p.status, kSiteLoraDone, p.wait_ns));
+    tc_fence_after();
+    if (warp < 4) {
+        float *row = part + (warp * 32 + lane) * C::kLd;
+#pragma unroll
+        for (int c = 0; c < R; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<float4 *>(row + c + e) =
+                    make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+        }
+    }
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmem);
+    }
+    if (warp < 4 && ok) {
+        // csize threads per row, each with every csize-th group of 4 columns
+        const int per = kShRows / (int)csize, mine = (int)threadIdx.x / (int)csize, sub = (int)threadIdx.x % (int)csize;
+        const int row = (int)crank * per + mine;
+        constexpr int kGroups = R / 4;
+        float top = 0.0f;
+        float *own = part + row * C::kLd;  // this row's part here is only read by its own threads from now on
+        for (int c = sub; c < kGroups; c += (int)csize) {
+            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (uint32_t z = 0; z < csize; ++z) {  // in rank order
+                const float4 v = ld_cluster_f4(mapa_shared(smem_u32(own + 4 * c), z));
+                a.x += v.x;
+                a.y += v.y;
+                a.z += v.z;
+                a.w += v.w;
+            }
+            // the columns behind the rank belong to another adapter
+            if (4 * c >= p.rank) a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            *reinterpret_cast<float4 *>(own + 4 * c) = a;
+            top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(a.z), fabsf(a.w)));
+        }
+        for (int o = 1; o < (int)csize; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        int e = (int)(__float_as_uint(top) >> 23) - 127;
+        e = e < -100 ? -100 : e > 126 ? 0 : e;
+        const float down = pow2f(-e);
+        if (row < count) {
+            T *h = static_cast<T *>(p.h) + (int64_t)(first + row) * 2 * R;
+            for (int c = sub; c < kGroups; c += (int)csize) {
+                const float4 a = *reinterpret_cast<const float4 *>(own + 4 * c);
+                const float v[4] = {a.x * down, a.y * down, a.z * down, a.w * down};
+                T hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    hi[j] = narrow<T>(v[j]);
+                    lo[j] = narrow<T>(v[j] - widen(hi[j]));
+                }
+                memcpy(h + 4 * c, hi, 8);
+                memcpy(h + R + 4 * c, lo, 8);
+            }
+            if (sub == 0) p.hscale[first + row] = pow2f(e);
+        }
+    }
+    cluster_sync();  // no CTA leaves while another reads its part
+}
+
+constexpr int kExRows = 64;
+
+template <typename T, int NB>
+__global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraParams p) {
+    constexpr int R = 8 * NB, kLd = R + 8;
+    __shared__ __align__(16) uint16_t hh[kExRows * kLd], hl[kExRows * kLd];
+    __shared__ int32_t off[kGroupsMax + 1];
+    __shared__ int32_t tile_s[3];
+    __shared__ int32_t row_s[kExRows];
+    __shared__ float scale_s[kExRows];
+    griddep_wait();
+    griddep_launch();
+    const int warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i <= p.groups; i += kLoraThreads) off[i] = p.offsets[i];
+    __syncthreads();
+    if (warp == 0) find_tile(off, p.groups, p.m, kExRows, (int)(blockIdx.x / p.nsplit), tile_s);
+    __syncthreads();
+    const int group = tile_s[0], first = tile_s[1], count = tile_s[2];
+    if (group == -2) return;  // reported by the first launch
+    if (group >= 0) {
+        if (threadIdx.x < kExRows) {
+            int32_t r = -1;
+            if ((int)threadIdx.x < count) {
+                r = p.rows[first + threadIdx.x];
+                if (r < 0 || r >= p.m) {
+                    record_status(p.status, kSiteBadRowIndex);
+                    r = -1;
+                }
+                scale_s[threadIdx.x] = (p.scales ? p.scales[group] : 1.0f) * p.hscale[first + threadIdx.x];
+            }
+            row_s[threadIdx.x] = r;
+        }
+        const uint4 *h = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.h) + (int64_t)first * 2 * R);
+        for (int i = threadIdx.x; i < kExRows * R / 4; i += kLoraThreads) {
+            const int row = i / (R / 4), c = i % (R / 4);  // 16-byte pieces: R / 8 of each term
+            const uint4 v = row < count ? h[i] : make_uint4(0, 0, 0, 0);
+            uint16_t *dst = c < R / 8 ? hh + row * kLd + 8 * c : hl + row * kLd + 8 * (c - R / 8);
+            *reinterpret_cast<uint4 *>(dst) = v;
+        }
+        __syncthreads();
+        expand_tile<T, kExRows / 16, NB>(p, group, row_s, scale_s, hh, hl, blockIdx.x % p.nsplit, p.nsplit);
+    }
+    copy_bare_rows<T>(p);
+}
+
+// Tiles of `rows` rows: a bound on sum ceil(rows of a group / rows).
+static int64_t tiles_bound(const LoraParams &p, int64_t rows) {
+    const int64_t t = p.m / rows + (p.groups < p.m ? p.groups : p.m);
+    return t < p.m ? t : p.m;
+}
+
+template <typename T, int NB>
+static sharq_status lora_two(LaunchCtx &ctx, LoraParams p) {
+    constexpr int R = 8 * NB;
+    using C = ShrinkCfg<R>;
+    CUtensorMap tm_x, tm_a;
+    if (!make_row_map(&tm_x, p.x, (uint64_t)p.k, (uint64_t)p.m, (uint64_t)p.ldx * 2, 1) ||
+        !make_row_map(&tm_a, p.a, (uint64_t)p.k, (uint64_t)p.groups * p.rank, (uint64_t)p.k * 2, R))
+        return SHARQ_ERR_CUDA;
+    SQ_SMEM_ONCE((lora_shrink_kernel<T, R>), C::kSmem);
+    const int64_t tiles = tiles_bound(p, kShRows);
+    int cluster = 1;
+    while (cluster < 8 && tiles * cluster < 2 * ctx.num_sms && p.k >= 2 * kShK * cluster) cluster *= 2;
+    sharq_status st = launch_pdl(ctx, lora_shrink_kernel<T, R>, tiles * cluster, kShThreads, C::kSmem, cluster, tm_x, tm_a, p);
+    if (st != SHARQ_OK) return st;
+    const int64_t ex = tiles_bound(p, kExRows);
+    p.nsplit = 1;
+    while (p.nsplit < 32 && ex * p.nsplit < 4 * ctx.num_sms && p.n >= 512 * p.nsplit) p.nsplit *= 2;
+    return launch_pdl(ctx, lora_expand_kernel<T, NB>, ex * p.nsplit, kLoraThreads, 0, 1, p);
+}
+
+// Whether a call takes the two-launch form (and so needs a workspace): rows
+// of an adapter, on average, beyond what a 16-row tile holds.
+static bool lora_many(int64_t m, int64_t groups) { return m > 16 * groups; }
+
+int64_t lora_ws_bytes(int64_t m, int64_t rank, int64_t groups) {
+    if (!lora_many(m, groups)) return 0;
+    return round_up(m * 4 * shrink_rank(rank), kAlign) + round_up(m * 4, kAlign);
 }
 
 template <typename T, int MT, int NB>
 static sharq_status lora_run(LaunchCtx &ctx, LoraParams p) {
     using C = LoraCfg<T, MT, NB>;
-    if (C::kSmem > 40 * 1024)
-        SQ_CUDA_TRY(cudaFuncSetAttribute(lora_kernel<T, MT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
-    const int64_t few = p.groups < p.m ? p.groups : p.m;
-    int64_t tiles = p.m / C::kRows + few;  // bound on sum ceil(rows of a group / kRows)
-    if (tiles > p.m) tiles = p.m;
+    SQ_SMEM_ONCE((lora_kernel<T, MT, NB>), C::kSmem);
+    const int64_t tiles = tiles_bound(p, C::kRows);
     // Split a tile until the CTAs fill the GPU twice, as long as a CTA keeps
     // a few hundred elements of k and of the columns.
     int cluster = 1;
@@ -378,22 +653,28 @@ static sharq_status lora_run(LaunchCtx &ctx, LoraParams p) {
 
 template <typename T>
 static sharq_status lora_any(LaunchCtx &ctx, const LoraParams &p) {
-    // rows of a group, on average, decide how many a tile holds; the
-    // accumulators of a warp (kRows x rank) decide how many it can hold
-    const bool many = p.m > 16 * (int64_t)p.groups;
-    if (p.rank <= 16) return many ? lora_run<T, 4, 2>(ctx, p) : lora_run<T, 1, 2>(ctx, p);
-    if (p.rank <= 32) return many ? lora_run<T, 4, 4>(ctx, p) : lora_run<T, 1, 4>(ctx, p);
-    if (p.rank <= 64) return many ? lora_run<T, 2, 8>(ctx, p) : lora_run<T, 1, 8>(ctx, p);
+    if (lora_many(p.m, p.groups)) {
+        switch (shrink_rank(p.rank)) {
+            case 16: return lora_two<T, 2>(ctx, p);
+            case 32: return lora_two<T, 4>(ctx, p);
+            case 64: return lora_two<T, 8>(ctx, p);
+            default: return lora_two<T, 16>(ctx, p);
+        }
+    }
+    if (p.rank <= 16) return lora_run<T, 1, 2>(ctx, p);
+    if (p.rank <= 32) return lora_run<T, 1, 4>(ctx, p);
+    if (p.rank <= 64) return lora_run<T, 1, 8>(ctx, p);
     return lora_run<T, 1, 16>(ctx, p);
 }
 
 sharq_status launch_lora(LaunchCtx &ctx, const void *x, int64_t ldx, int64_t m, int64_t k, const void *a, const void *b,
                          int64_t n, int64_t rank, int64_t groups, const float *scales, const int32_t *offsets,
                          const int32_t *rows, const int32_t *slots, int dtype, const void *base, int64_t ldbase, void *out,
-                         int64_t ldo) {
+                         int64_t ldo, void *ws) {
     if (m == 0) return SHARQ_OK;
     LoraParams p{x, a, b, base, scales, out, offsets, rows, slots, ldx, ldbase, ldo, m,
-                 (int32_t)k, (int32_t)n, (int32_t)rank, (int32_t)groups, 1, ctx.status};
+                 (int32_t)k, (int32_t)n, (int32_t)rank, (int32_t)groups, 1, ctx.status, ctx.wait_ns, ws,
+                 reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + round_up(m * 4 * shrink_rank(rank), kAlign))};
     return dtype == SHARQ_F16 ? lora_any<__half>(ctx, p) : lora_any<__nv_bfloat16>(ctx, p);
 }
 

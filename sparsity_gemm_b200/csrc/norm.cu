@@ -30,6 +30,21 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     if (lane == 0) red[warp] = v;
     __syncthreads();
+    if (warps <= 8) {  // reading all of them takes fewer instructions than shuffles
+        const float4 a = reinterpret_cast<const float4 *>(red)[0];
+        float s = a.x;
+        if (warps > 1) s += a.y;
+        if (warps > 2) s += a.z;
+        if (warps > 3) s += a.w;
+        if (warps > 4) {
+            const float4 b = reinterpret_cast<const float4 *>(red)[1];
+            s += b.x;
+            if (warps > 5) s += b.y;
+            if (warps > 6) s += b.z;
+            if (warps > 7) s += b.w;
+        }
+        return s;
+    }
     return warp_sum(lane < warps ? red[lane] : 0.0f);
 }
 
@@ -46,6 +61,83 @@ struct NormParams {
     int32_t rms;
 };
 
+// Steps on one vector of a row, on packed pairs of binary32 where it holds an
+// even number of values (half the instructions; the pass is issue-bound
+// otherwise).
+template <typename T, int VW>
+struct Row {
+    using V = Vec<T, VW>;
+    using P = typename V::P;
+    static __device__ __forceinline__ float sum(P v) {
+        if constexpr (VW > 1) {
+            uint64_t f[VW / 2];
+            V::unpack2(v, f);
+            uint64_t s = f[0];
+#pragma unroll
+            for (int e = 1; e < VW / 2; ++e) s = add2(s, f[e]);
+            const float2 t = up2(s);
+            return t.x + t.y;
+        } else {
+            float f[VW];
+            V::unpack(v, f);
+            return f[0];
+        }
+    }
+    // sum of (x - mu)^2
+    static __device__ __forceinline__ float sum_squares(P v, float mu) {
+        if constexpr (VW > 1) {
+            uint64_t f[VW / 2], q = pk2(0.0f, 0.0f);
+            const uint64_t m = pk2(-mu, -mu);
+            V::unpack2(v, f);
+#pragma unroll
+            for (int e = 0; e < VW / 2; ++e) {
+                const uint64_t d = add2(f[e], m);
+                q = fma2(d, d, q);
+            }
+            const float2 t = up2(q);
+            return t.x + t.y;
+        } else {
+            float f[VW];
+            V::unpack(v, f);
+            return (f[0] - mu) * (f[0] - mu);
+        }
+    }
+    // (x - mu) rstd w + b of vector c
+    static __device__ __forceinline__ P apply(P v, float mu, float rstd, const T *w, const T *b, int c) {
+        if constexpr (VW > 1) {
+            uint64_t f[VW / 2], g[VW / 2];
+            const uint64_t m = pk2(-mu, -mu), r = pk2(rstd, rstd);
+            V::unpack2(v, f);
+#pragma unroll
+            for (int e = 0; e < VW / 2; ++e) f[e] = mul2(add2(f[e], m), r);
+            if (w) {
+                V::unpack2(V::load(w + (int64_t)c * VW), g);
+#pragma unroll
+                for (int e = 0; e < VW / 2; ++e) f[e] = mul2(f[e], g[e]);
+            }
+            if (b) {
+                V::unpack2(V::load(b + (int64_t)c * VW), g);
+#pragma unroll
+                for (int e = 0; e < VW / 2; ++e) f[e] = add2(f[e], g[e]);
+            }
+            return V::pack2(f);
+        } else {
+            float f[VW], g[VW];
+            V::unpack(v, f);
+            f[0] = (f[0] - mu) * rstd;
+            if (w) {
+                V::unpack(V::load(w + c), g);
+                f[0] *= g[0];
+            }
+            if (b) {
+                V::unpack(V::load(b + c), g);
+                f[0] += g[0];
+            }
+            return V::pack(f);
+        }
+    }
+};
+
 // A row lives in the registers of its threads (NV vectors of VW elements
 // each, vector i of a thread at i * threads + thread), so x is read once.
 // WARP: one warp per row, kFwdWarps rows per CTA; else one CTA per row.
@@ -54,7 +146,8 @@ constexpr int kFwdWarps = 4;
 template <typename T, int VW, int NV, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kFwdWarps : 1024) norm_fwd_kernel(const NormParams p) {
     using V = Vec<T, VW>;
-    __shared__ float red[2][32];
+    using R = Row<T, VW>;
+    __shared__ __align__(16) float red[2][32];
     griddep_wait();
     griddep_launch();
     const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
@@ -77,28 +170,16 @@ __global__ void __launch_bounds__(WARP ? 32 * kFwdWarps : 1024) norm_fwd_kernel(
     if (!p.rms) {
         float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float f[VW];
-            V::unpack(xv[i], f);
-#pragma unroll
-            for (int e = 0; e < VW; ++e) s += f[e];
-        }
+        for (int i = 0; i < NV; ++i) s += R::sum(xv[i]);
         mu = row_sum<WARP>(s, red[0]) * inv_k;
     }
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (i * threads + tid < nvec) {
-            float f[VW];
-            V::unpack(xv[i], f);
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const float d = f[e] - mu;
-                q = fmaf(d, d, q);
-            }
-        }
+        const float d = R::sum_squares(xv[i], mu);
+        if (i * threads + tid < nvec) q += d;
     }
-    const float rstd = 1.0f / sqrtf(row_sum<WARP>(q, red[1]) * inv_k + p.eps);
+    const float rstd = rsqrtf(row_sum<WARP>(q, red[1]) * inv_k + p.eps);
     if (tid == 0) {
         if (p.mean) p.mean[row] = mu;
         if (p.rstd) p.rstd[row] = rstd;
@@ -106,23 +187,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kFwdWarps : 1024) norm_fwd_kernel(
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = i * threads + tid;
-        if (c < nvec) {
-            float f[VW], wf[VW], bf[VW];
-            V::unpack(xv[i], f);
-#pragma unroll
-            for (int e = 0; e < VW; ++e) f[e] = (f[e] - mu) * rstd;
-            if (w) {
-                V::unpack(V::load(w + (int64_t)c * VW), wf);
-#pragma unroll
-                for (int e = 0; e < VW; ++e) f[e] *= wf[e];
-            }
-            if (b) {
-                V::unpack(V::load(b + (int64_t)c * VW), bf);
-#pragma unroll
-                for (int e = 0; e < VW; ++e) f[e] += bf[e];
-            }
-            V::store(y + (int64_t)c * VW, V::pack(f));
-        }
+        if (c < nvec) V::store(y + (int64_t)c * VW, R::apply(xv[i], mu, rstd, w, b, c));
     }
 }
 
@@ -133,7 +198,7 @@ constexpr int kLongThreads = 1024;
 template <typename T, int VW>
 __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(const NormParams p) {
     using V = Vec<T, VW>;
-    __shared__ float red[2][32];
+    __shared__ __align__(16) float red[2][32];
     griddep_wait();
     griddep_launch();
     const int64_t row = blockIdx.x;
@@ -141,47 +206,23 @@ __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(const NormP
     const T *x = static_cast<const T *>(p.x) + row * p.k;
     T *y = static_cast<T *>(p.y) + row * p.k;
     const T *w = static_cast<const T *>(p.w), *b = static_cast<const T *>(p.b);
+    using R = Row<T, VW>;
     const float inv_k = 1.0f / (float)p.k;
-    float mu = 0.0f, f[VW], wf[VW];
+    float mu = 0.0f;
     if (!p.rms) {
         float s = 0.0f;
-        for (int c = threadIdx.x; c < nvec; c += kLongThreads) {
-            V::unpack(V::load(x + (int64_t)c * VW), f);
-#pragma unroll
-            for (int e = 0; e < VW; ++e) s += f[e];
-        }
+        for (int c = threadIdx.x; c < nvec; c += kLongThreads) s += R::sum(V::load(x + (int64_t)c * VW));
         mu = row_sum<false>(s, red[0]) * inv_k;
     }
     float q = 0.0f;
-    for (int c = threadIdx.x; c < nvec; c += kLongThreads) {
-        V::unpack(V::load(x + (int64_t)c * VW), f);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-            const float d = f[e] - mu;
-            q = fmaf(d, d, q);
-        }
-    }
-    const float rstd = 1.0f / sqrtf(row_sum<false>(q, red[1]) * inv_k + p.eps);
+    for (int c = threadIdx.x; c < nvec; c += kLongThreads) q += R::sum_squares(V::load(x + (int64_t)c * VW), mu);
+    const float rstd = rsqrtf(row_sum<false>(q, red[1]) * inv_k + p.eps);
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mu;
         if (p.rstd) p.rstd[row] = rstd;
     }
-    for (int c = threadIdx.x; c < nvec; c += kLongThreads) {
-        V::unpack(V::load(x + (int64_t)c * VW), f);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) f[e] = (f[e] - mu) * rstd;
-        if (w) {
-            V::unpack(V::load(w + (int64_t)c * VW), wf);
-#pragma unroll
-            for (int e = 0; e < VW; ++e) f[e] *= wf[e];
-        }
-        if (b) {
-            V::unpack(V::load(b + (int64_t)c * VW), wf);
-#pragma unroll
-            for (int e = 0; e < VW; ++e) f[e] += wf[e];
-        }
-        V::store(y + (int64_t)c * VW, V::pack(f));
-    }
+    for (int c = threadIdx.x; c < nvec; c += kLongThreads)
+        V::store(y + (int64_t)c * VW, R::apply(V::load(x + (int64_t)c * VW), mu, rstd, w, b, c));
 }
 
 // ---------------------------------------------------------------------------
@@ -201,8 +242,8 @@ struct NormBwdParams {
     const void *dy, *x, *w;
     const float *mean, *rstd;
     void *dx;
-    float *part;  // [parts][2][k] (dw, then db), NULL: no weight gradients
-    int64_t rows;
+    float *part;  // [parts][part_cols]: dw, then db (LayerNorm); NULL: no weight gradients
+    int64_t rows, part_cols;
     int32_t k, parts, rms;
 };
 
@@ -336,13 +377,13 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
                 }
         }
         __syncthreads();
-        for (int c = threadIdx.x; c < 2 * p.k; c += blockDim.x) {
+        for (int c = threadIdx.x; c < p.part_cols; c += blockDim.x) {
             float s = 0.0f;
             for (int g = 0; g < kBwdWarps; ++g) s += acc_sm[(int64_t)g * 2 * p.k + c];
-            p.part[(int64_t)blockIdx.x * 2 * p.k + c] = s;
+            p.part[(int64_t)blockIdx.x * p.part_cols + c] = s;
         }
     } else {
-        float *mine = p.part + (int64_t)part * 2 * p.k;
+        float *mine = p.part + (int64_t)part * p.part_cols;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = i * threads + tid;
@@ -350,28 +391,190 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
 #pragma unroll
                 for (int e = 0; e < VW; ++e) {
                     mine[c * VW + e] = dw[i * VW + e];
-                    mine[p.k + c * VW + e] = db[i * VW + e];
+                    if (!p.rms) mine[p.k + c * VW + e] = db[i * VW + e];
                 }
         }
     }
 }
 
+// The form for rows of whole 16-byte vectors: a CTA (or a cluster, each CTA
+// with its part of the columns) per row, kBwdCols columns per thread, and a
+// ring of rows of x and dy filled by bulk copies several rows ahead. The
+// barrier of a row's reduction also frees its ring slot.
+#ifndef BWD_OCC
+#define BWD_OCC 2
+#endif
+constexpr int kRingMax = 8;            // most rows in a ring
+constexpr int kRingBytes = 160 << 10;  // shared memory of an SM's rings
+
+#ifndef RCOLS
+#define RCOLS 16
+#endif
+#ifndef RMAXT
+#define RMAXT 256
+#endif
+template <typename T, int VW, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT <= RMAXT ? BWD_OCC : 1)
+    norm_bwd_ring_kernel(const NormBwdParams p, int stages, uint64_t wait_ns, unsigned *status) {
+    using V = Vec<T, VW>;
+    constexpr int NV = RCOLS / VW, H = VW / 2;
+    extern __shared__ __align__(128) uint8_t ring[];  // [stages][x, dy][part of a row]
+    __shared__ uint64_t full[kRingMax];
+    __shared__ __align__(16) float2 red[2][MAXT / 32];
+    __shared__ float2 peer[2][kBwdCluster];
+    griddep_wait();
+    griddep_launch();
+    const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t crank = cluster_ctarank();
+    uint32_t csize;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
+    const int per = (p.k / VW + (int)csize - 1) / (int)csize;  // vectors of a CTA
+    const int v0 = (int)crank * per, cnt = max(0, min(per, p.k / VW - v0));
+    const uint32_t bytes = (uint32_t)cnt * 16, stride = (uint32_t)per * 16;
+    const int64_t part = blockIdx.x / csize, parts = gridDim.x / csize;
+    const int iters = (int)((p.rows - part + parts - 1) / parts);
+    const T *xp = static_cast<const T *>(p.x) + (int64_t)v0 * VW, *dyp = static_cast<const T *>(p.dy) + (int64_t)v0 * VW;
+    const T *wp = static_cast<const T *>(p.w);
+    T *dxp = static_cast<T *>(p.dx) + (int64_t)v0 * VW;
+    auto issue = [&](int it, int s) {
+        const int64_t at = (part + it * parts) * p.k;
+        const uint32_t dst = smem_u32(ring) + s * 2 * stride, bar = smem_u32(&full[s]);
+        mbar_arrive_expect_tx(bar, 2 * bytes);
+        if (bytes) {
+            bulk_load(dst, xp + at, bytes, bar);
+            bulk_load(dst + stride, dyp + at, bytes, bar);
+        }
+    };
+    if (tid == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&full[s]), 1);
+        mbar_fence_init();
+    }
+    if (tid < 2 * (MAXT / 32)) red[tid / (MAXT / 32)][tid % (MAXT / 32)] = make_float2(0.0f, 0.0f);  // warps not there
+    __syncthreads();
+    if (csize > 1) cluster_sync();  // every CTA of the row runs before another writes to its shared memory
+    if (tid == 0)
+        for (int it = 0; it < stages && it < iters; ++it) issue(it, it);
+    const float inv_k = 1.0f / (float)p.k;
+    typename V::P wv[NV];
+    uint64_t dw[NV][H], db[NV][H];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * threads + tid;
+        wv[i] = wp && c < cnt ? V::load(wp + (int64_t)(v0 + c) * VW) : V::ones();
+#pragma unroll
+        for (int e = 0; e < H; ++e) dw[i][e] = db[i][e] = 0;
+    }
+    float mu_n = p.rms || iters <= 0 ? 0.0f : p.mean[part], rs_n = iters <= 0 ? 0.0f : p.rstd[part];
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int it = 0; it < iters; ++it) {
+        const int64_t row = part + it * parts;
+        const float mu = mu_n, rs = rs_n;
+        if (it + 1 < iters) {
+            if (!p.rms) mu_n = __ldg(p.mean + row + parts);
+            rs_n = __ldg(p.rstd + row + parts);
+        }
+        const uint64_t mu2 = pk2(-mu, -mu), rs2 = pk2(rs, rs);
+        (void)mbar_wait_own(smem_u32(&full[slot]), phase, status, kSiteNormRing, wait_ns);
+        uint64_t h[NV][H], g[NV][H], t1 = 0, t2 = 0;  // xhat and g = dy w; sums of g and g xhat
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * threads + tid;
+            const uint8_t *at = ring + slot * 2 * stride + c * 16;
+            uint64_t df[H], wf[H];
+            // columns past the row: dy = 0, so they add nothing
+            V::unpack2(c < cnt ? *reinterpret_cast<const typename V::P *>(at) : V::zero(), h[i]);
+            V::unpack2(c < cnt ? *reinterpret_cast<const typename V::P *>(at + stride) : V::zero(), df);
+            V::unpack2(wv[i], wf);
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+                h[i][e] = mul2(add2(h[i][e], mu2), rs2);
+                dw[i][e] = fma2(df[e], h[i][e], dw[i][e]);
+                db[i][e] = add2(db[i][e], df[e]);
+                g[i][e] = mul2(df[e], wf[e]);
+                t1 = add2(t1, g[i][e]);
+                t2 = fma2(g[i][e], h[i][e], t2);
+            }
+        }
+        const float2 f1 = up2(t1), f2 = up2(t2);
+        // lanes 0-15 go on with the first sum, lanes 16-31 with the second
+        float s1 = f1.x + f1.y, s2 = f2.x + f2.y;
+        float v = (lane & 16 ? s2 : s1) + __shfl_xor_sync(0xFFFFFFFFu, lane & 16 ? s1 : s2, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        const int parity = it & 1;
+        if (lane == 0) red[parity][warp].x = v;
+        if (lane == 16) red[parity][warp].y = v;
+        __syncthreads();
+        if (tid == 0 && it + stages < iters) issue(it + stages, slot);
+        s1 = s2 = 0.0f;
+        const float4 *rp = reinterpret_cast<const float4 *>(red[parity]);
+#pragma unroll
+        for (int i = 0; i < MAXT / 64; ++i) {
+            const float4 r = rp[i];
+            s1 += r.x + r.z;
+            s2 += r.y + r.w;
+        }
+        if (csize > 1) {  // every CTA of the row gets every CTA's sums, added in rank order
+            if ((uint32_t)tid < csize) {
+                const uint32_t at = mapa_shared(smem_u32(&peer[parity][crank]), (uint32_t)tid);
+                st_cluster_u32(at, __float_as_uint(s1));
+                st_cluster_u32(at + 4, __float_as_uint(s2));
+            }
+            cluster_sync();
+            s1 = s2 = 0.0f;
+            for (uint32_t c = 0; c < csize; ++c) {
+                s1 += peer[parity][c].x;
+                s2 += peer[parity][c].y;
+            }
+        }
+        const float m1 = p.rms ? 0.0f : s1 * inv_k, m2 = s2 * inv_k;
+        const uint64_t m1n = pk2(-m1 * rs, -m1 * rs), m2n = pk2(-m2, -m2);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * threads + tid;
+#pragma unroll
+            for (int e = 0; e < H; ++e) g[i][e] = fma2(fma2(h[i][e], m2n, g[i][e]), rs2, m1n);
+            if (c < cnt) V::store(dxp + row * p.k + (int64_t)c * VW, V::pack2(g[i]));
+        }
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    if (!p.part) return;
+    float *mine = p.part + part * p.part_cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * threads + tid;
+        if (c < cnt)
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+                *reinterpret_cast<float2 *>(mine + (v0 + c) * VW + 2 * e) = up2(dw[i][e]);
+                if (!p.rms) *reinterpret_cast<float2 *>(mine + p.k + (v0 + c) * VW + 2 * e) = up2(db[i][e]);
+            }
+    }
+}
+
 // dw and db: column sums of the partial rows. A CTA takes 32 columns; its 32
 // warps add every 32nd partial row, then the 32 sums are added in order.
-__global__ void __launch_bounds__(1024) norm_bwd_reduce_kernel(const float *part, int parts, int k, float *dw, float *db) {
+__global__ void __launch_bounds__(1024) norm_bwd_reduce_kernel(const float *part, int parts, int64_t cols, int k, float *dw,
+                                                               float *db) {
     __shared__ float sum[32][33];
     griddep_wait();
     griddep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;  // column of [dw | db]
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;  // column of [dw | db]
     float s = 0.0f;
-    if (c < 2 * k)
-        for (int r = warp; r < parts; r += 32) s += part[(int64_t)r * 2 * k + c];
+    if (c < cols) {
+#pragma unroll 4
+        for (int r = warp; r < parts; r += 32) s += part[r * cols + c];
+    }
     sum[warp][lane] = s;
     __syncthreads();
     const float t = warp_sum(sum[lane][warp]);  // column blockIdx.x * 32 + warp
-    const int o = blockIdx.x * 32 + warp;
-    if (lane == 0 && o < 2 * k) {
+    const int64_t o = (int64_t)blockIdx.x * 32 + warp;
+    if (lane == 0 && o < cols) {
         if (o < k) {
             if (dw) dw[o] = t;
         } else if (db) {
@@ -391,7 +594,6 @@ static sharq_status norm_fwd(LaunchCtx &ctx, const NormParams &p) {
     const int64_t warp_grid = (p.rows + kFwdWarps - 1) / kFwdWarps;
     if (nvec <= 32) return launch_pdl(ctx, norm_fwd_kernel<T, VW, 1, true>, warp_grid, 32 * kFwdWarps, 0, 1, p);
     if (nvec <= 128) return launch_pdl(ctx, norm_fwd_kernel<T, VW, 4, true>, warp_grid, 32 * kFwdWarps, 0, 1, p);
-    if (nvec <= 2048) return launch_pdl(ctx, norm_fwd_kernel<T, VW, 2, false>, p.rows, threads_for(nvec, 2), 0, 1, p);
     if (nvec <= 4096) return launch_pdl(ctx, norm_fwd_kernel<T, VW, 4, false>, p.rows, threads_for(nvec, 4), 0, 1, p);
     return launch_pdl(ctx, norm_fwd_long_kernel<T, VW>, p.rows, kLongThreads, 0, 1, p);
 }
@@ -406,8 +608,25 @@ sharq_status launch_layer_norm(LaunchCtx &ctx, const void *x, int64_t rows, int6
     });
 }
 
-// Partial rows of the weight gradients (a workspace size, so a function of
-// the shape alone).
+// CTAs of a row in the backward pass, threads of such a CTA, and how many of
+// them an SM holds.
+static int bwd_cluster(int64_t k) {
+    int c = 1;
+    while ((int64_t)c * kBwdThreads * kBwdCols < k) c *= 2;
+    return c;
+}
+static int bwd_threads(int64_t k, int cluster) {
+    return (int)round_up(((k + RCOLS - 1) / RCOLS + cluster - 1) / cluster, 32);
+}
+static int bwd_per_sm(int threads) {
+    if (threads > RMAXT) return 1;
+    const int n = BWD_OCC * RMAXT / threads;
+    return n > 8 ? 8 : n;
+}
+
+// Row groups of the backward pass, each with a partial row of the weight
+// gradients (a workspace size, so a function of the shape alone). A group has
+// some rows to itself, or the partial rows outweigh the pass.
 int64_t norm_bwd_parts(int64_t rows, int64_t k) {
     if (rows <= 0) return 0;
     const int64_t sms = 148;
@@ -415,9 +634,10 @@ int64_t norm_bwd_parts(int64_t rows, int64_t k) {
         const int64_t need = (rows + kBwdWarps - 1) / kBwdWarps;
         return need < 2 * sms ? need : 2 * sms;
     }
-    const int64_t per_sm = k <= 4096 ? 3 : k <= 8192 ? 2 : 1;
-    const int64_t most = k <= 8192 ? per_sm * sms : sms * 8192 / round_up(k, 8192);
-    return rows < most ? rows : most;
+    const int cluster = bwd_cluster(k);
+    const int64_t most = bwd_per_sm(bwd_threads(k, cluster)) * sms / cluster;
+    const int64_t few = rows <= 64 ? rows : rows / 6 < 64 ? 64 : rows / 6;
+    return few < most ? few : most;
 }
 
 template <typename T, int VW>
@@ -426,11 +646,22 @@ static sharq_status norm_bwd(LaunchCtx &ctx, const NormBwdParams &p) {
         const size_t smem = (size_t)kBwdWarps * 2 * p.k * sizeof(float);  // at most 32 KB
         return launch_pdl(ctx, norm_bwd_kernel<T, VW, true>, p.parts, 32 * kBwdWarps, smem, 1, p);
     }
-    int cluster = 1;
-    while ((int64_t)cluster * kBwdThreads * kBwdCols < p.k) cluster *= 2;
-    const int nvec = p.k / VW, nv = kBwdCols / VW;
-    const int threads = (int)round_up(((nvec + nv - 1) / nv + cluster - 1) / cluster, 32);
-    return launch_pdl(ctx, norm_bwd_kernel<T, VW, false>, (int64_t)p.parts * cluster, threads, 0, cluster, p);
+    const int cluster = bwd_cluster(p.k), threads = bwd_threads(p.k, cluster);
+    if constexpr (VW > 1) {
+        const int64_t pair = 2 * 16 * ((p.k / VW + cluster - 1) / cluster);
+        const int64_t fit = kRingBytes / bwd_per_sm(threads) / pair;
+        const int stages = fit > kRingMax ? kRingMax : (int)fit;  // at least 2: a pair of rows has at most 64 KB
+        if (threads <= RMAXT) {
+            SQ_SMEM_ONCE((norm_bwd_ring_kernel<T, VW, RMAXT>), kRingBytes);
+            return launch_pdl(ctx, norm_bwd_ring_kernel<T, VW, RMAXT>, (int64_t)p.parts * cluster, threads,
+                              (size_t)(stages * pair), cluster, p, stages, ctx.wait_ns, ctx.status);
+        }
+        SQ_SMEM_ONCE((norm_bwd_ring_kernel<T, VW, 1024 * 8 / RCOLS>), kRingBytes);
+        return launch_pdl(ctx, norm_bwd_ring_kernel<T, VW, 1024 * 8 / RCOLS>, (int64_t)p.parts * cluster, threads,
+                          (size_t)(stages * pair), cluster, p, stages, ctx.wait_ns, ctx.status);
+    } else {
+        return launch_pdl(ctx, norm_bwd_kernel<T, VW, false>, (int64_t)p.parts * cluster, threads, 0, cluster, p);
+    }
 }
 
 sharq_status launch_layer_norm_backward(LaunchCtx &ctx, const void *dy, const void *x, int64_t rows, int64_t k,
@@ -438,8 +669,9 @@ sharq_status launch_layer_norm_backward(LaunchCtx &ctx, const void *dy, const vo
                                         void *dx, float *dw, float *db, float *part, bool vec16) {
     const int parts = (int)norm_bwd_parts(rows, k);
     const bool grads = dw || db;
+    const int64_t cols = norm == 1 ? k : 2 * k;  // RMSNorm has no db
     if (rows > 0) {
-        NormBwdParams p{dy, x, w, mean, rstd, dx, grads ? part : nullptr, rows, (int32_t)k, parts, norm};
+        NormBwdParams p{dy, x, w, mean, rstd, dx, grads ? part : nullptr, rows, cols, (int32_t)k, parts, norm};
         const sharq_status st = with_dtype(dtype, [&](auto t) {
             using T = decltype(t);
             return vec16 ? norm_bwd<T, 16 / (int)sizeof(T)>(ctx, p) : norm_bwd<T, 1>(ctx, p);
@@ -447,7 +679,7 @@ sharq_status launch_layer_norm_backward(LaunchCtx &ctx, const void *dy, const vo
         if (st != SHARQ_OK) return st;
     }
     if (!grads) return SHARQ_OK;
-    return launch_pdl(ctx, norm_bwd_reduce_kernel, (2 * k + 31) / 32, 1024, 0, 1, (const float *)part, parts, (int)k, dw, db);
+    return launch_pdl(ctx, norm_bwd_reduce_kernel, (cols + 31) / 32, 1024, 0, 1, (const float *)part, parts, cols, (int)k, dw, db);
 }
 
 }  // namespace sq

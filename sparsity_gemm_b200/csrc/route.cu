@@ -158,9 +158,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
 template <typename ID>
 static sharq_status route_run(LaunchCtx &ctx, const RouteParams &p) {
     const size_t smem = (size_t)(kRouteWarps + 1) * p.groups * sizeof(int32_t);
-    if (smem > 46 * 1024)
-        SQ_CUDA_TRY(cudaFuncSetAttribute(route_kernel<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)((kRouteWarps + 1) * kGroupsMax * sizeof(int32_t))));
+    SQ_SMEM_ONCE(route_kernel<ID>, (kRouteWarps + 1) * kGroupsMax * sizeof(int32_t));
     int ctas = 1;
     while (ctas < kRouteCluster && p.entries > (int64_t)ctas * kRouteThreads * 2) ctas *= 2;
     return launch_pdl(ctx, route_kernel<ID>, ctas, kRouteThreads, smem, ctas, p);

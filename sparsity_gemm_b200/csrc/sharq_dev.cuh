@@ -368,6 +368,24 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigne
     }
 }
 
+// The same wait ended by its own limit only (not by a status that another call
+// left behind); returns whether the phase completed.
+__device__ __forceinline__ bool mbar_wait_own(uint32_t bar, uint32_t parity, unsigned *status, unsigned site,
+                                              uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0 && globaltimer_ns() - t0 > limit_ns) {
+            record_status(status, site);
+            return false;
+        }
+    }
+}
+
+// Wait sites of the 16/32-bit operators.
+enum : unsigned { kSiteNormRing = 0x141, kSiteLoraFull = 0x142, kSiteLoraEmpty = 0x143, kSiteLoraDone = 0x144 };
+
 // ---------------------------------------------------------------------------
 // Grouped (mixture-of-experts) launches. Group g owns grouped rows
 // offsets[g] .. offsets[g+1]-1 and, in a grouped prep, the 128-row tiles
@@ -429,6 +447,17 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tmap, int3
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+// Four rows (r0 .. r3) of a 2-D tensor whose map has one-row boxes, from
+// column c0 on, one after another in shared memory.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const void *tmap, int32_t c0, int32_t r0, int32_t r1, int32_t r2,
+                                            int32_t r3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
         : "memory");
 }
 
@@ -547,6 +576,17 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo_bytes,
     d |= 1ull << 46;
     d |= (uint64_t)layout << 61;
     return d;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit operands of one type, binary32
+// accumulator.
+__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T with per-16 UE4M3 block scales (NVFP4).

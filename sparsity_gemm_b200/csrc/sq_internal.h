@@ -1,5 +1,6 @@
 // Host-side declarations shared by the library's translation units.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -38,6 +39,9 @@ sharq_status launch_linear_grouped(LaunchCtx &ctx, const sharq_prep &P, const sh
 sharq_status launch_gather(LaunchCtx &ctx, const sharq_prep &S, const int32_t *row_idx, const int32_t *offsets,
                            int32_t groups, int64_t rows, const sharq_prep &D);
 sharq_status launch_wait_probe(LaunchCtx &ctx, uint64_t limit_ns);
+// 2-D map of 16-bit elements [rows][cols] with a row stride in bytes; box =
+// 64 elements x box_rows, 128-byte swizzle.
+bool make_row_map(CUtensorMap *tm, const void *base, uint64_t cols, uint64_t rows, uint64_t ld_bytes, uint32_t box_rows);
 // Records the kernel count that sharq_last_launch_count reports.
 void note_launches(int n);
 sharq_status launch_div_check(LaunchCtx &ctx, uint64_t count, uint64_t seed, uint64_t *mismatches, float *examples);
@@ -65,7 +69,9 @@ sharq_status launch_combine_backward(LaunchCtx &ctx, const void *dout, const voi
 sharq_status launch_lora(LaunchCtx &ctx, const void *x, int64_t ldx, int64_t m, int64_t k, const void *a, const void *b,
                          int64_t n, int64_t rank, int64_t groups, const float *scales, const int32_t *offsets,
                          const int32_t *rows, const int32_t *slots, int dtype, const void *base, int64_t ldbase, void *out,
-                         int64_t ldo);
+                         int64_t ldo, void *ws);
+// Workspace of launch_lora in bytes (0: none).
+int64_t lora_ws_bytes(int64_t m, int64_t rank, int64_t groups);
 
 }  // namespace sq
 

@@ -8,6 +8,10 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+#include <type_traits>
+
+#include "sharq_dev.cuh"
 #include "sq_internal.h"
 
 namespace sq {
@@ -36,6 +40,24 @@ __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_
 template <>
 __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+template <typename T>
+struct IsBf16 { static constexpr bool v = false; };
+template <>
+struct IsBf16<__nv_bfloat16> { static constexpr bool v = true; };
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    uint32_t w;
+    memcpy(&w, &h, 4);
+    return w;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    uint32_t w;
+    memcpy(&w, &h, 4);
+    return w;
+}
+
 template <typename T, int VW>
 struct Vec {
     using P = typename Packed<VW * (int)sizeof(T)>::type;
@@ -43,6 +65,12 @@ struct Vec {
         P p;
         memset(&p, 0, sizeof(p));
         return p;
+    }
+    static __device__ __forceinline__ P ones() {
+        float f[VW];
+#pragma unroll
+        for (int i = 0; i < VW; ++i) f[i] = 1.0f;
+        return pack(f);
     }
     static __device__ __forceinline__ P load(const T *p) { return __ldg(reinterpret_cast<const P *>(p)); }
     static __device__ __forceinline__ void store(T *p, P v) { *reinterpret_cast<P *>(p) = v; }
@@ -52,12 +80,40 @@ struct Vec {
 #pragma unroll
         for (int i = 0; i < VW; ++i) f[i] = widen(t[i]);
     }
-    static __device__ __forceinline__ P pack(const float (&f)[VW]) {
-        T t[VW];
+    // The same as packed binary32 pairs (VW even).
+    static __device__ __forceinline__ void unpack2(P v, uint64_t (&f)[(VW + 1) / 2]) {
+        uint32_t w[sizeof(P) / 4 ? sizeof(P) / 4 : 1];
+        memcpy(w, &v, sizeof(v));
 #pragma unroll
-        for (int i = 0; i < VW; ++i) t[i] = narrow<T>(f[i]);
+        for (int i = 0; i < VW / 2; ++i) {
+            if constexpr (sizeof(T) == 4) f[i] = (uint64_t)w[2 * i] | (uint64_t)w[2 * i + 1] << 32;
+            else if constexpr (sizeof(T) == 2 && !IsBf16<T>::v) f[i] = h2_to_f2(w[i]);
+            else f[i] = pk2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+        }
+    }
+    static __device__ __forceinline__ P pack2(const uint64_t (&f)[(VW + 1) / 2]) {
+        float t[VW];
+#pragma unroll
+        for (int i = 0; i < VW / 2; ++i) {
+            const float2 u = up2(f[i]);
+            t[2 * i] = u.x;
+            t[2 * i + 1] = u.y;
+        }
+        return pack(t);
+    }
+    static __device__ __forceinline__ P pack(const float (&f)[VW]) {
         P v;
-        memcpy(&v, t, sizeof(v));
+        if constexpr (sizeof(T) == 2 && VW % 2 == 0) {  // two values per conversion
+            uint32_t w[VW / 2];
+#pragma unroll
+            for (int i = 0; i < VW / 2; ++i) w[i] = IsBf16<T>::v ? bf16x2(f[2 * i], f[2 * i + 1]) : f16x2(f[2 * i], f[2 * i + 1]);
+            memcpy(&v, w, sizeof(v));
+        } else {
+            T t[VW];
+#pragma unroll
+            for (int i = 0; i < VW; ++i) t[i] = narrow<T>(f[i]);
+            memcpy(&v, t, sizeof(v));
+        }
         return v;
     }
 };
@@ -76,11 +132,23 @@ static inline sharq_status with_dtype(int dtype, F f) {
     return f(float());
 }
 
+// Raises a kernel's dynamic shared memory limit, once per device.
+#define SQ_SMEM_ONCE(kernel, bytes)                                                                              \
+    do {                                                                                                         \
+        static std::atomic<uint64_t> _done{0};                                                                   \
+        int _dev = 0;                                                                                            \
+        SQ_CUDA_TRY(cudaGetDevice(&_dev));                                                                       \
+        if (!((_done.load() >> _dev) & 1u)) {                                                                    \
+            SQ_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(bytes))); \
+            _done.fetch_or(1ull << _dev);                                                                        \
+        }                                                                                                        \
+    } while (0)
+
 // Launch with programmatic stream serialization (the kernels start with
 // griddep_wait) and, for cluster > 1, a cluster dimension.
-template <typename P, typename... A>
-static sharq_status launch_pdl(LaunchCtx &ctx, void (*kernel)(P, A...), int64_t grid, int threads, size_t smem, int cluster,
-                               P p, A... a) {
+template <typename... A>
+static sharq_status launch_pdl(LaunchCtx &ctx, void (*kernel)(A...), int64_t grid, int threads, size_t smem, int cluster,
+                               std::common_type_t<A>... a) {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
@@ -96,7 +164,7 @@ static sharq_status launch_pdl(LaunchCtx &ctx, void (*kernel)(P, A...), int64_t 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    SQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, p, a...));
+    SQ_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, a...));
     ctx.launches++;
     return SHARQ_OK;
 }

@@ -87,8 +87,8 @@ def test_moves_refusals(L):
 
 def test_lora_refusals(L):
     def call(x=P(1), ldx=256, m=10, k=256, a=P(2), b=P(3), n=128, r=16, g=4, s=P(4), off=P(5), rows=P(6), slots=P(7), dt=0,
-             base=P(8), ldb=128, out=P(9), ldo=128):
-        return L.sharq_lora(x, ldx, m, k, a, b, n, r, g, s, off, rows, slots, dt, base, ldb, out, ldo, None)
+             base=P(8), ldb=128, out=P(9), ldo=128, ws=None, nws=0):
+        return L.sharq_lora(x, ldx, m, k, a, b, n, r, g, s, off, rows, slots, dt, base, ldb, out, ldo, ws, nws, None)
 
     for bad in (dict(k=252, ldx=252), dict(n=124), dict(r=12), dict(r=0), dict(r=136), dict(g=0), dict(g=1025), dict(m=-1),
                 dict(ldx=248), dict(ldx=260), dict(ldo=120), dict(ldo=132), dict(ldb=64), dict(ldb=1 << 25), dict(x=None),
@@ -96,6 +96,10 @@ def test_lora_refusals(L):
                 dict(base=P(8, 8)), dict(out=P(9, 8)), dict(s=P(4, 2)), dict(dt=3), dict(out=P(1)), dict(out=P(8, 16)),
                 dict(out=P(8), ldo=256), dict(out=P(2)), dict(out=P(3, 16)), dict(k=65544, ldx=65544), dict(n=(1 << 20) + 8)):
         assert call(**bad) == sq.ERR_INVALID_ARG, bad
+    need = L.sharq_lora_bytes(4096, 16, 4)
+    assert need >= 4096 * 64 and L.sharq_lora_bytes(10, 16, 4) == 0 and L.sharq_lora_bytes(4096, 136, 4) == 0
+    for bad in (dict(ws=None, nws=need), dict(ws=P(10), nws=need - 1), dict(ws=P(10, 64), nws=need)):
+        assert call(m=4096, **bad) == sq.ERR_INVALID_ARG, bad
     assert call(dt=2) == sq.ERR_UNSUPPORTED
     assert call(m=0) == sq.OK
     # slices of one buffer whose columns overlap are refused, like whole ones
@@ -113,6 +117,7 @@ def here(monkeypatch):
     that records its calls."""
     fake = mock.MagicMock()
     fake.sharq_layer_norm_backward_bytes.return_value = 4096
+    fake.sharq_lora_bytes.return_value = 0
     for name in ("layer_norm", "layer_norm_backward", "route", "permute_rows", "combine", "combine_backward", "lora"):
         getattr(fake, "sharq_" + name).return_value = sq.OK
     monkeypatch.setattr(sq, "lib", lambda: fake)
