@@ -639,7 +639,7 @@ sharq_status sharq_combine_backward(const void *dout_dev, const void *y_dev, int
  * multiples of 8, buffers 16-byte aligned; rank <= SHARQ_RANK_MAX, n_out <=
  * 2^20, n_groups <= SHARQ_GROUPS_MAX. Column slices of one buffer are fine as
  * x, base or out where their columns are disjoint.
- * Invalid offsets write nothing, invalid rows are skipped; both are reported
+ * Invalid offsets leave the groups' rows unwritten, invalid rows are skipped; both are reported
  * by sharq_get_last_error as SHARQ_ERR_INVALID_ARG.
  *   ws_dev    workspace of sharq_lora_bytes(m_tok, rank, n_groups) bytes,
  *             256-byte aligned; NULL where that is 0 (few rows per adapter).

@@ -12,6 +12,7 @@ Inference" (arXiv 2606.26587), Abstract.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import numpy as np
@@ -540,52 +541,88 @@ def linear_grouped(prep: Prepared, offsets: torch.Tensor, qw: QuantizedWeight, r
 
 # ---------------------------------------------------------------------------
 # Operators around the FP4 linear in 16 or 32 bits
+#
+# These calls are short, so their checks are too: one test per tensor, and a
+# second look, which says what is wrong, only where it fails.
 
 F16, BF16, F32 = 0, 1, 2
 TOP_K_MAX, RANK_MAX, GROUPS_MAX = 64, 128, 1024
 _DTYPES = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+_f32, _i32 = torch.float32, torch.int32
 
 
-def _matrix(t: torch.Tensor, name: str, dtype=None, shape=None, strided: bool = False):
-    """t is a CUDA matrix of a supported type (of `dtype` and `shape` where
-    given): contiguous, or with rows of consecutive elements if strided."""
-    _require(isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in _DTYPES,
-             f"{name} must be an fp16, bf16 or fp32 matrix")
+def _refuse(t, name: str, dev: int, dtype, shape, rows: bool):
+    """Raises ValueError with what is wrong with t (see _take)."""
+    kind = "vector" if len(shape) == 1 else "matrix" if len(shape) == 2 else f"tensor with {len(shape)} dimensions"
+    _require(isinstance(t, torch.Tensor) and t.dim() == len(shape), f"{name} must be a {kind}")
     _require(dtype is None or t.dtype == dtype, f"{name} must be of type {dtype}")
-    _require(shape is None or tuple(t.shape) == tuple(shape), f"{name} must have the shape {tuple(shape or ())}")
-    if strided:
+    _require(dtype is not None or t.dtype in _DTYPES, f"{name} must be of type fp16, bf16 or fp32")
+    _require(all(w is None or w == s for s, w in zip(t.shape, shape)), f"{name} must have the shape {tuple(shape)}")
+    if rows:
         _require(t.numel() == 0 or ((t.stride(1) == 1 or t.shape[1] == 1)
                                     and (t.stride(0) >= t.shape[1] or t.shape[0] == 1)),
                  f"the rows of {name} must hold consecutive elements and not overlap")
     else:
         _require(t.is_contiguous(), f"{name} must be contiguous")
     _cuda_here(t, name)
+    _require(t.get_device() == dev, f"{name} must be on the device of the first argument")
 
 
-def _vector(t: torch.Tensor, name: str, dtype, n: int):
-    _require(isinstance(t, torch.Tensor) and t.dtype == dtype and t.dim() == 1 and t.is_contiguous() and t.numel() == n,
-             f"{name} must be a contiguous vector of {n} elements of type {dtype}")
-    _cuda_here(t, name)
+def _first(t, name: str, dims: int = 2, rows: bool = False, dtype=None) -> int:
+    """Checks the tensor that fixes a call's type and device; the device."""
+    if not (isinstance(t, torch.Tensor) and t.dim() == dims and (t.dtype in _DTYPES if dtype is None else t.dtype == dtype)
+            and (rows or t.is_contiguous()) and t.is_cuda and t.get_device() == torch.cuda.current_device()):
+        _refuse(t, name, t.get_device() if isinstance(t, torch.Tensor) else -1, dtype, (None,) * dims, rows)
+    return t.get_device()
+
+
+def _take(t, name: str, dev: int, dtype, shape, rows: bool = False):
+    """Checks a tensor: device, type, shape, and contiguous (rows: rows of
+    consecutive elements that do not overlap)."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype == dtype and t.shape == shape
+            and t.is_contiguous()):
+        _refuse(t, name, dev, dtype, shape, rows)
 
 
 def _no_grad_inputs(*ts):
     """The calls below are not recorded by autograd; a call that would lose a
     gradient silently is refused (the *_backward calls are the gradients)."""
-    _require(not (torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in ts)),
-             "inputs that require a gradient are refused: call under torch.no_grad() and use the backward calls")
+    if torch.is_grad_enabled():
+        for t in ts:
+            _require(t is None or not t.requires_grad,
+                     "inputs that require a gradient are refused: call under torch.no_grad() and use the backward calls")
 
 
-def _empty(shape, dtype, device, stream):
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
     """A new tensor that belongs to the stream its kernel runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Row stride in elements (a single row has none of its own)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+def _new_like(t: torch.Tensor, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _raw(stream, dev: int) -> int:
+    """The stream to launch on."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    _require(stream.device_index == dev, f"stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_kind(norm: str) -> int:
+    _require(norm == "layer" or norm == "rms", 'norm must be "layer" or "rms"')
+    return 1 if norm == "rms" else 0
 
 
 def layer_norm(x: torch.Tensor, w=None, b=None, eps: float = 1e-5, norm: str = "layer", stats: bool = False,
@@ -594,23 +631,34 @@ def layer_norm(x: torch.Tensor, w=None, b=None, eps: float = 1e-5, norm: str = "
     b) of x [m_tok, k] (fp16, bf16 or fp32): x's type, rounded once. With
     stats=True returns (y, mean, rstd) for layer_norm_backward: fp32 [m_tok],
     mean None for RMSNorm."""
-    _require(norm in ("layer", "rms") and (norm == "layer" or b is None),
-             'norm must be "layer" or "rms" (RMSNorm takes no b)')
-    _matrix(x, "x")
+    kind = _norm_kind(norm)
+    dev = _first(x, "x")
     m_tok, k = x.shape
-    for t, name in ((w, "w"), (b, "b")):
-        if t is not None:
-            _vector(t, name, x.dtype, k)
+    dt = x.dtype
+    if w is not None:
+        _take(w, "w", dev, dt, (k,))
+    if b is not None:
+        _require(kind == 0, "RMSNorm takes no b")
+        _take(b, "b", dev, dt, (k,))
     _no_grad_inputs(x, w, b)
     if out is None:
-        out = _empty((m_tok, k), x.dtype, x.device, stream)
-    _matrix(out, "out", x.dtype, x.shape)
-    mean = _empty((m_tok,), torch.float32, x.device, stream) if stats and norm == "layer" else None
-    rstd = _empty((m_tok,), torch.float32, x.device, stream) if stats else None
-    _check(lib().sharq_layer_norm(_ptr(x), m_tok, k, _ptr(w), _ptr(b), float(eps), 1 if norm == "rms" else 0,
-                                  _DTYPES[x.dtype], _ptr(out), _ptr(mean), _ptr(rstd), _stream(stream)),
-           "sharq_layer_norm")
+        out = _new_like(x, stream)
+    else:
+        _take(out, "out", dev, dt, (m_tok, k))
+    mean = rstd = None
+    if stats:
+        mean = _new(x, (m_tok,), _f32, stream) if kind == 0 else None
+        rstd = _new(x, (m_tok,), _f32, stream)
+    st = lib().sharq_layer_norm(x.data_ptr(), m_tok, k, _at(w), _at(b), eps, kind, _DTYPES[dt], out.data_ptr(), _at(mean),
+                                _at(rstd), _raw(stream, dev))
+    if st:
+        _check(st, "sharq_layer_norm")
     return (out, mean, rstd) if stats else out
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_backward_bytes(m_tok: int, k: int) -> int:
+    return int(lib().sharq_layer_norm_backward_bytes(m_tok, k))
 
 
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean, rstd: torch.Tensor, w=None, norm: str = "layer",
@@ -619,32 +667,35 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean, rstd: torch.Ten
     mean (None for RMSNorm), rstd and w. dx has x's type (out: where to put it,
     may be dy itself); dw and db are fp32 [k], None without w, and db None for
     RMSNorm."""
-    _require(norm in ("layer", "rms") and (norm == "layer") == (mean is not None),
-             'norm must be "layer" (with mean) or "rms" (mean None)')
-    _matrix(x, "x")
-    _matrix(dy, "dy", x.dtype, x.shape)
+    kind = _norm_kind(norm)
+    _require((kind == 0) == (mean is not None), 'norm "layer" takes a mean, "rms" none')
+    dev = _first(x, "x")
     m_tok, k = x.shape
+    dt = x.dtype
+    _take(dy, "dy", dev, dt, (m_tok, k))
     if mean is not None:
-        _vector(mean, "mean", torch.float32, m_tok)
-    _vector(rstd, "rstd", torch.float32, m_tok)
+        _take(mean, "mean", dev, _f32, (m_tok,))
+    _take(rstd, "rstd", dev, _f32, (m_tok,))
     if w is not None:
-        _vector(w, "w", x.dtype, k)
+        _take(w, "w", dev, dt, (k,))
     _no_grad_inputs(dy, x, w)
     if out is None:
-        out = _empty((m_tok, k), x.dtype, x.device, stream)
-    _matrix(out, "out", x.dtype, x.shape)
+        out = _new_like(x, stream)
+    else:
+        _take(out, "out", dev, dt, (m_tok, k))
     dw = db = ws = None
     nbytes = 0
     if w is not None:
-        nbytes = int(lib().sharq_layer_norm_backward_bytes(m_tok, k))
+        nbytes = _norm_backward_bytes(m_tok, k)
         if nbytes == 0:
             raise SharqError(ERR_INVALID_ARG, f"layer_norm_backward shape {tuple(x.shape)}")
-        dw = _empty((k,), torch.float32, x.device, stream)
-        db = _empty((k,), torch.float32, x.device, stream) if norm == "layer" else None
-        ws = _empty((nbytes,), torch.uint8, x.device, stream)
-    _check(lib().sharq_layer_norm_backward(_ptr(dy), _ptr(x), m_tok, k, _ptr(w), _ptr(mean), _ptr(rstd),
-                                           1 if norm == "rms" else 0, _DTYPES[x.dtype], _ptr(out), _ptr(dw), _ptr(db),
-                                           _ptr(ws), nbytes, _stream(stream)), "sharq_layer_norm_backward")
+        dw = _new(x, (k,), _f32, stream)
+        db = _new(x, (k,), _f32, stream) if kind == 0 else None
+        ws = _new(x, (nbytes,), torch.uint8, stream)
+    st = lib().sharq_layer_norm_backward(dy.data_ptr(), x.data_ptr(), m_tok, k, _at(w), _at(mean), rstd.data_ptr(), kind,
+                                         _DTYPES[dt], out.data_ptr(), _at(dw), _at(db), _at(ws), nbytes, _raw(stream, dev))
+    if st:
+        _check(st, "sharq_layer_norm_backward")
     return out, dw, db
 
 
@@ -655,50 +706,41 @@ class Routing:
     none). Made once, it serves every call of the step that sorts by the same
     ids."""
 
+    __slots__ = ("offsets", "rows", "slots", "groups", "m_tok", "top_k", "dev")
+
     def __init__(self, offsets: torch.Tensor, rows: torch.Tensor, slots: torch.Tensor):
-        _int32_vector(offsets, "offsets")
-        _int32_vector(rows, "rows")
-        _require(isinstance(slots, torch.Tensor) and slots.dtype == torch.int32 and slots.dim() == 2
-                 and slots.is_contiguous(), "slots must be a contiguous int32 matrix")
-        _cuda_here(slots, "slots")
-        _require(offsets.numel() >= 2 and rows.numel() == slots.numel() and slots.shape[1] >= 1,
-                 "rows must hold one element per element of slots, offsets one more than there are groups")
+        self.dev = dev = _first(slots, "slots", 2, False, _i32)
+        self.m_tok, self.top_k = slots.shape
+        self.groups = offsets.numel() - 1
+        _take(offsets, "offsets", dev, _i32, (self.groups + 1,))
+        _take(rows, "rows", dev, _i32, (self.m_tok * self.top_k,))
+        _require(self.groups >= 1 and self.top_k >= 1, "a routing has at least one group and one entry per token")
         self.offsets, self.rows, self.slots = offsets, rows, slots
 
-    @property
-    def groups(self) -> int:
-        return self.offsets.numel() - 1
 
-    @property
-    def m_tok(self) -> int:
-        return self.slots.shape[0]
-
-    @property
-    def top_k(self) -> int:
-        return self.slots.shape[1]
-
-
-def _routing(r, m_tok=None):
+def _routing(r, dev: int):
     _require(isinstance(r, Routing), "routing must be a Routing (from route)")
-    _cuda_here(r.offsets, "routing.offsets")
-    _require(m_tok is None or r.m_tok == m_tok, f"routing is of {r.m_tok} tokens, not {m_tok}")
+    _require(r.dev == dev, f"routing is on cuda:{r.dev}, the tensors on cuda:{dev}")
 
 
 def route(ids: torch.Tensor, groups: int, stream=None) -> Routing:
     """Entries sorted by group, on the GPU: ids [m_tok, top_k] (or [m_tok]),
     int32 or int64, holds each entry's expert or adapter; an id outside 0 ..
     groups - 1 (-1, say) means none. Entries of a group keep their order."""
-    _require(isinstance(ids, torch.Tensor) and ids.dtype in (torch.int32, torch.int64) and ids.dim() in (1, 2)
-             and ids.is_contiguous(), "ids must be a contiguous int32 or int64 matrix (or vector)")
-    _cuda_here(ids, "ids")
+    _require(isinstance(ids, torch.Tensor) and ids.dtype in (_i32, torch.int64) and ids.dim() in (1, 2),
+             "ids must be an int32 or int64 matrix (or vector)")
+    dev = _first(ids, "ids", ids.dim(), False, ids.dtype)
     m_tok, top_k = ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1
-    _require(1 <= top_k <= TOP_K_MAX and 1 <= groups <= GROUPS_MAX,
-             f"route takes 1 to {TOP_K_MAX} ids per token and 1 to {GROUPS_MAX} groups")
-    r = Routing(_empty((groups + 1,), torch.int32, ids.device, stream),
-                _empty((m_tok * top_k,), torch.int32, ids.device, stream),
-                _empty((m_tok, top_k), torch.int32, ids.device, stream))
-    _check(lib().sharq_route(_ptr(ids), ids.element_size(), m_tok, top_k, groups, _ptr(r.offsets), _ptr(r.rows),
-                             _ptr(r.slots), _stream(stream)), "sharq_route")
+    _require(1 <= top_k <= TOP_K_MAX and 1 <= groups <= GROUPS_MAX, "too many ids per token, or groups, or none")
+    r = Routing.__new__(Routing)
+    r.dev, r.m_tok, r.top_k, r.groups = dev, m_tok, top_k, groups
+    r.offsets = _new(ids, (groups + 1,), _i32, stream)
+    r.rows = _new(ids, (m_tok * top_k,), _i32, stream)
+    r.slots = _new(ids, (m_tok, top_k), _i32, stream)
+    st = lib().sharq_route(ids.data_ptr(), ids.element_size(), m_tok, top_k, groups, r.offsets.data_ptr(),
+                           r.rows.data_ptr(), r.slots.data_ptr(), _raw(stream, dev))
+    if st:
+        _check(st, "sharq_route")
     return r
 
 
@@ -706,16 +748,21 @@ def permute_rows(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = N
     """Rows of x [m_tok, k] in grouped order: [m_tok * top_k, k], row
     slots[t, j] = x[t], zero behind the last group (what prepare_grouped and
     the grouped products read). Its gradient is combine(dy, routing)."""
-    _matrix(x, "x")
-    _routing(routing, x.shape[0])
+    dev = _first(x, "x")
+    _routing(routing, dev)
+    m_tok, k = x.shape
+    _require(routing.m_tok == m_tok, "routing is of another number of tokens")
     _no_grad_inputs(x)
-    shape = (routing.rows.numel(), x.shape[1])
+    shape = (m_tok * routing.top_k, k)
     if out is None:
-        out = _empty(shape, x.dtype, x.device, stream)
-    _matrix(out, "out", x.dtype, shape)
-    _check(lib().sharq_permute_rows(_ptr(x), x.shape[0], x.shape[1], _ptr(routing.slots), routing.top_k,
-                                    _ptr(routing.offsets), routing.groups, _DTYPES[x.dtype], _ptr(out),
-                                    _stream(stream)), "sharq_permute_rows")
+        out = _new(x, shape, x.dtype, stream)
+    else:
+        _take(out, "out", dev, x.dtype, shape)
+    st = lib().sharq_permute_rows(x.data_ptr(), m_tok, k, routing.slots.data_ptr(), routing.top_k,
+                                  routing.offsets.data_ptr(), routing.groups, _DTYPES[x.dtype], out.data_ptr(),
+                                  _raw(stream, dev))
+    if st:
+        _check(st, "sharq_permute_rows")
     return out
 
 
@@ -724,19 +771,23 @@ def combine(y: torch.Tensor, routing: Routing, weights: torch.Tensor | None = No
     """Grouped rows y [rows, k] back to their tokens: [m_tok, k] with row t =
     residual[t] + sum_j weights[t, j] y[slots[t, j]] (weights fp32 [m_tok,
     top_k], None: 1). out may be residual itself."""
-    _matrix(y, "y")
-    _routing(routing)
-    m_tok, k = routing.m_tok, y.shape[1]
-    _no_grad_inputs(y, weights, residual)
+    dev = _first(y, "y")
+    _routing(routing, dev)
+    m_tok, top_k, dt = routing.m_tok, routing.top_k, y.dtype
+    rows, k = y.shape
     if weights is not None:
-        _matrix(weights, "weights", torch.float32, (m_tok, routing.top_k))
+        _take(weights, "weights", dev, _f32, (m_tok, top_k))
     if residual is not None:
-        _matrix(residual, "residual", y.dtype, (m_tok, k))
+        _take(residual, "residual", dev, dt, (m_tok, k))
+    _no_grad_inputs(y, weights, residual)
     if out is None:
-        out = _empty((m_tok, k), y.dtype, y.device, stream)
-    _matrix(out, "out", y.dtype, (m_tok, k))
-    _check(lib().sharq_combine(_ptr(y), y.shape[0], m_tok, k, _ptr(routing.slots), _ptr(weights), routing.top_k,
-                               _ptr(residual), _DTYPES[y.dtype], _ptr(out), _stream(stream)), "sharq_combine")
+        out = _new(y, (m_tok, k), dt, stream)
+    else:
+        _take(out, "out", dev, dt, (m_tok, k))
+    st = lib().sharq_combine(y.data_ptr(), rows, m_tok, k, routing.slots.data_ptr(), _at(weights), top_k, _at(residual),
+                             _DTYPES[dt], out.data_ptr(), _raw(stream, dev))
+    if st:
+        _check(st, "sharq_combine")
     return out
 
 
@@ -745,18 +796,26 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, routing: Routing, weig
     rows y and the weights. dy [rows, k] is zero behind the last group;
     dweights is fp32 [m_tok, top_k], 0 where an entry has no group. The
     residual's gradient is dout."""
-    _matrix(y, "y")
-    _routing(routing)
-    m_tok, k = routing.m_tok, y.shape[1]
-    _matrix(dout, "dout", y.dtype, (m_tok, k))
-    _matrix(weights, "weights", torch.float32, (m_tok, routing.top_k))
+    dev = _first(y, "y")
+    _routing(routing, dev)
+    m_tok, top_k, dt = routing.m_tok, routing.top_k, y.dtype
+    rows, k = y.shape
+    _take(dout, "dout", dev, dt, (m_tok, k))
+    _take(weights, "weights", dev, _f32, (m_tok, top_k))
     _no_grad_inputs(dout, y, weights)
-    dy = _empty(tuple(y.shape), y.dtype, y.device, stream)
-    dweights = _empty((m_tok, routing.top_k), torch.float32, y.device, stream)
-    _check(lib().sharq_combine_backward(_ptr(dout), _ptr(y), y.shape[0], m_tok, k, _ptr(routing.slots), _ptr(weights),
-                                        routing.top_k, _ptr(routing.offsets), routing.groups, _DTYPES[y.dtype],
-                                        _ptr(dy), _ptr(dweights), _stream(stream)), "sharq_combine_backward")
+    dy = _new_like(y, stream)
+    dweights = _new_like(weights, stream)
+    st = lib().sharq_combine_backward(dout.data_ptr(), y.data_ptr(), rows, m_tok, k, routing.slots.data_ptr(),
+                                      weights.data_ptr(), top_k, routing.offsets.data_ptr(), routing.groups, _DTYPES[dt],
+                                      dy.data_ptr(), dweights.data_ptr(), _raw(stream, dev))
+    if st:
+        _check(st, "sharq_combine_backward")
     return dy, dweights
+
+
+@functools.lru_cache(maxsize=4096)
+def _lora_bytes(m_tok: int, rank: int, groups: int) -> int:
+    return int(lib().sharq_lora_bytes(m_tok, rank, groups))
 
 
 def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, routing: Routing, scales: torch.Tensor | None = None,
@@ -769,36 +828,45 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, routing: Routing, sc
       the rows' adapters ([m_tok] or [m_tok, 1]); scales fp32 [adapters].
     base is the shared projection's output, e.g. linear()'s; out may be base
     itself, and x, base and out may be column slices (rows strided)."""
-    _matrix(x, "x", strided=True)
-    _require(x.dtype != torch.float32, "x must be an fp16 or bf16 matrix")
-    for t, name in ((a, "a"), (b, "b")):
-        _require(isinstance(t, torch.Tensor) and t.dim() == 3 and t.dtype == x.dtype and t.is_contiguous(),
-                 f"{name} must be a contiguous tensor of x's type with 3 dimensions")
-        _cuda_here(t, name)
+    dev = _first(x, "x", 2, True)
+    dt = x.dtype
+    _require(dt != _f32, "x must be an fp16 or bf16 matrix")
     m_tok, k = x.shape
-    groups, n_out, rank = b.shape
-    _require(tuple(a.shape) == (groups, rank, k), f"a must have the shape {(groups, rank, k)}")
+    if not x.is_contiguous():
+        _take(x, "x", dev, dt, (m_tok, k), True)
+    _routing(routing, dev)
+    groups = routing.groups
+    _require(isinstance(b, torch.Tensor) and b.dim() == 3, "b must be a tensor with 3 dimensions")
+    _, n_out, rank = b.shape
+    _take(b, "b", dev, dt, (groups, n_out, rank))
+    _take(a, "a", dev, dt, (groups, rank, k))
     _require(k % 8 == 0 and n_out % 8 == 0 and rank % 8 == 0 and 8 <= rank <= RANK_MAX and k > 0 and n_out > 0,
-             f"k, n_out and rank must be multiples of 8, rank at most {RANK_MAX}")
-    _routing(routing, m_tok)
-    _require(routing.top_k == 1 and routing.groups == groups, "routing must give each row one of the adapters")
+             "k, n_out and rank must be multiples of 8, rank at most 128")
+    _require(routing.top_k == 1 and routing.m_tok == m_tok, "routing must give each row of x one of the adapters")
     if scales is not None:
-        _vector(scales, "scales", torch.float32, groups)
+        _take(scales, "scales", dev, _f32, (groups,))
+    ldbase = 0
     if base is not None:
-        _matrix(base, "base", x.dtype, (m_tok, n_out), strided=True)
+        _take(base, "base", dev, dt, (m_tok, n_out), True)
+        ldbase = base.stride(0) if m_tok > 1 else n_out
     _no_grad_inputs(x, a, b, scales, base)
     if out is None:
-        out = _empty((m_tok, n_out), x.dtype, x.device, stream)
-    _matrix(out, "out", x.dtype, (m_tok, n_out), strided=True)
-    lds = [_ld(t) if t is not None else 0 for t in (x, base, out)]
-    _require(all(v % 8 == 0 for v in lds) and all(t is None or t.data_ptr() % 16 == 0 for t in (x, a, b, base, out)),
+        out = _new(x, (m_tok, n_out), dt, stream)
+        ldo = n_out
+    else:
+        _take(out, "out", dev, dt, (m_tok, n_out), True)
+        ldo = out.stride(0) if m_tok > 1 else n_out
+    ldx = x.stride(0) if m_tok > 1 else k
+    px, pa, pb, pbase, pout = x.data_ptr(), a.data_ptr(), b.data_ptr(), _at(base), out.data_ptr()
+    _require((ldx | ldbase | ldo) % 8 == 0 and (px | pa | pb | (pbase or 0) | pout) % 16 == 0,
              "x, a, b, base and out must be 16-byte aligned, with row strides that are multiples of 8")
-    nbytes = int(lib().sharq_lora_bytes(m_tok, rank, groups))
-    ws = _empty((nbytes,), torch.uint8, x.device, stream) if nbytes else None
-    _check(lib().sharq_lora(_ptr(x), lds[0], m_tok, k, _ptr(a), _ptr(b), n_out, rank, groups, _ptr(scales),
-                            _ptr(routing.offsets), _ptr(routing.rows), _ptr(routing.slots), _DTYPES[x.dtype],
-                            _ptr(base), lds[1], _ptr(out), lds[2], _ptr(ws), nbytes, _stream(stream)),
-           "sharq_lora")
+    nbytes = _lora_bytes(m_tok, rank, groups)
+    ws = _new(x, (nbytes,), torch.uint8, stream) if nbytes else None
+    st = lib().sharq_lora(px, ldx, m_tok, k, pa, pb, n_out, rank, groups, _at(scales), routing.offsets.data_ptr(),
+                          routing.rows.data_ptr(), routing.slots.data_ptr(), _DTYPES[dt], pbase, ldbase, pout, ldo,
+                          _at(ws), nbytes, _raw(stream, dev))
+    if st:
+        _check(st, "sharq_lora")
     return out
 
 

@@ -40,10 +40,11 @@ struct LoraParams {
     const float *scales;
     void *out;
     const int32_t *offsets, *rows, *slots;
-    int64_t ldx, ldbase, ldo;
+    int32_t ldx, ldbase, ldo;
     int64_t m;
     int32_t k, n, rank, groups;
     int32_t nsplit;  // clusters (expand: CTAs) that share a tile, each with its part of the columns
+    int32_t bare_ctas;  // CTAs, the grid's first, that copy rows without a group
     unsigned *status;
     uint64_t wait_ns;
     void *h;         // two-launch form: [grouped row][2][padded rank] 16-bit terms
@@ -63,11 +64,25 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with nothing to add to.
+template <typename T>
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    const float z = 0.0f;
+    if constexpr (IsBf16<T>::v)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z));
+}
+
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) { return __uint_as_float(ld_cluster_u32(addr)); }
 
-// The tile's group and rows, found by warp 0 in the offsets (in shared
-// memory). tile_s: [0] group (-1: no such tile, -2: bad offsets), [1] first
-// grouped row, [2] rows.
+// The tile's group and rows, found by warp 0 in the offsets. tile_s: [0] group
+// (-1: no such tile, -2: bad offsets), [1] first grouped row, [2] rows.
 __device__ __forceinline__ void find_tile(const int32_t *off, int groups, int64_t m, int tile_rows, int tile,
                                           int32_t *tile_s) {
     const int lane = threadIdx.x & 31;
@@ -106,110 +121,211 @@ __device__ __forceinline__ void find_tile(const int32_t *off, int groups, int64_
     }
 }
 
-// out = base + scale h B^T for the tile's rows, over piece `piece` of `pieces`
-// of the blocks of 32 columns; warps take turns. hh, hl: the two terms of h.
-template <typename T, int MT, int NB>
+// First tile of every group, tiles[groups] their number, by one warp from the
+// offsets in shared memory. Returns, in every lane, whether these are valid.
+__device__ __forceinline__ bool build_tiles(const int32_t *off, int groups, int64_t m, int tile_rows, int32_t *tiles) {
+    const int lane = threadIdx.x & 31;
+    bool ok = off[0] == 0 && off[groups] <= m;
+    int32_t carry = 0;
+    if (lane == 0) tiles[0] = 0;
+    for (int base = 0; base < groups; base += 32) {
+        const int g = base + lane;
+        int32_t t = 0;
+        if (g < groups) {
+            const int32_t a = off[g], b = off[g + 1];
+            if (b < a || a < 0 || b > m) ok = false;
+            else t = (b - a + tile_rows - 1) / tile_rows;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t v = __shfl_up_sync(0xFFFFFFFFu, t, o);
+            if (lane >= o) t += v;
+        }
+        if (g < groups) tiles[g + 1] = carry + t;
+        carry += __shfl_sync(0xFFFFFFFFu, t, 31);
+    }
+    return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// find_tile for the whole CTA. Up to 32 groups are read by their lanes; more go
+// through shared memory (off), so that they are all in flight at once.
+__device__ __forceinline__ void cta_find_tile(const LoraParams &p, int32_t *off, int tile_rows, int tile, int32_t *tile_s) {
+    const int32_t *from = p.offsets;
+    if (p.groups > 32) {
+        for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) off[i] = p.offsets[i];
+        __syncthreads();
+        from = off;
+    }
+    if (threadIdx.x < 32) find_tile(from, p.groups, p.m, tile_rows, tile, tile_s);
+    __syncthreads();
+}
+
+// out = base + scale h B^T for the tile's rows, over the blocks c0 .. c1-1 of 32
+// columns; warps take turns. hh, hl: the two terms of h.
+// A lane reads base for the very elements it writes, so the next blocks' are on
+// their way into `ahead` (written and read by that thread alone) while a block
+// is computed; B's part of the next block is on its way into registers. ready()
+// runs after the first of these loads and before h is read.
+constexpr int kAhead = 2;
+
+template <int MT>
+constexpr int kAheadBytes = kAhead * 2 * MT * 16 * kLoraThreads;
+
+template <typename T, int MT, int NB, typename F>
 __device__ __forceinline__ void expand_tile(const LoraParams &p, int group, const int32_t *row_s, const float *scale_s,
-                                            const uint16_t *hh, const uint16_t *hl, int64_t piece, int64_t pieces) {
-    constexpr int kLd = 8 * NB + 8;
+                                            const uint16_t *hh, const uint16_t *hl, uint8_t *ahead, int c0, int c1,
+                                            F ready) {
+    constexpr int kLd = 8 * NB + 8, kS = (NB + 3) / 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
-            const T *b = static_cast<const T *>(p.b) + (int64_t)group * p.n * p.rank;
-            const T *base = static_cast<const T *>(p.base);
-            T *out = static_cast<T *>(p.out);
-            const int blocks = (p.n + 31) / 32;
-            const int c0 = (int)(blocks * piece / pieces), c1 = (int)(blocks * (piece + 1) / pieces);
-            for (int c = c0 + warp; c < c1; c += kLoraWarps) {
-                const int n0 = 32 * c, col = n0 + 8 * q;
-                uint4 bv[4][(NB + 3) / 4];
-    #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int row = n0 + 8 * (g8 >> 1) + 2 * j + (g8 & 1);
-                    const T *br = b + (int64_t)row * p.rank;
-    #pragma unroll
-                    for (int s = 0; s < (NB + 3) / 4; ++s) {
-                        bv[j][s] = make_uint4(0, 0, 0, 0);
-                        if (NB == 2) {  // one step of 16
-                            if (row < p.n && 4 * q < p.rank) {
-                                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(br + 4 * q));
-                                bv[j][s].x = v.x;
-                                bv[j][s].y = v.y;
-                            }
-                        } else if (row < p.n && 32 * s + 8 * q < p.rank) {
-                            bv[j][s] = __ldg(reinterpret_cast<const uint4 *>(br + 32 * s + 8 * q));
-                        }
+    const T *b = static_cast<const T *>(p.b) + (int64_t)group * p.n * p.rank;
+    const T *base = static_cast<const T *>(p.base);
+    T *out = static_cast<T *>(p.out);
+    uint4 *mine = reinterpret_cast<uint4 *>(ahead) + threadIdx.x;
+    int32_t row[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) row[i][h] = row_s[16 * i + 8 * h + g8];
+    const uint32_t slots = smem_u32(mine);
+    auto fetch = [&](int c, int s) {
+        const int col = 32 * c + 8 * q;
+        if (base && c < c1 && col < p.n) {
+            const T *at = base + col;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (row[i][h] >= 0)
+                        cp_async16(slots + (uint32_t)(((s * MT + i) * 2 + h) * kLoraThreads * 16),
+                                   at + (int64_t)row[i][h] * p.ldbase);
+        }
+        cp_async_commit();
+    };
+    // this lane's rows of B in a block of 32: bl + 2 j; 8 of them end inside n or not at all
+    const int bl = 8 * (g8 >> 1) + (g8 & 1);
+    const T *b_lane = b + (int64_t)bl * p.rank + (NB == 2 ? 4 : 8) * q;
+    auto fetch_b = [&](int c, uint4 (&v)[4][kS]) {
+        const bool in = c < c1 && 32 * c + bl < p.n;
+        const T *at = b_lane + (int64_t)c * (32 * p.rank);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int s = 0; s < kS; ++s) {
+                v[j][s] = make_uint4(0, 0, 0, 0);
+                if (NB == 2) {  // one step of 16
+                    if (in && 4 * q < p.rank) {
+                        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(at + 2 * j * p.rank));
+                        v[j][s].x = w.x;
+                        v[j][s].y = w.y;
                     }
+                } else if (in && 32 * s + 8 * q < p.rank) {
+                    v[j][s] = __ldg(reinterpret_cast<const uint4 *>(at + 2 * j * p.rank + 32 * s));
                 }
-                uint4 old[MT][2];
-    #pragma unroll
-                for (int i = 0; i < MT; ++i)
-    #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int32_t r = row_s[16 * i + 8 * h + g8];
-                        old[i][h] = make_uint4(0, 0, 0, 0);
-                        if (base && r >= 0 && col < p.n)
-                            old[i][h] = *reinterpret_cast<const uint4 *>(base + (int64_t)r * p.ldbase + col);
-                    }
-    #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    float d[4][4];
-    #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-    #pragma unroll
-                        for (int e = 0; e < 4; ++e) d[j][e] = 0.0f;
-    #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const uint16_t *hp = (z ? hl : hh) + (16 * i + g8) * kLd;
-    #pragma unroll
-                        for (int s = 0; s < (NB + 3) / 4; ++s) {
-                            if (NB == 2) {
-                                const uint2 h0 = *reinterpret_cast<const uint2 *>(hp + 4 * q);
-                                const uint2 h1 = *reinterpret_cast<const uint2 *>(hp + 8 * kLd + 4 * q);
-    #pragma unroll
-                                for (int j = 0; j < 4; ++j) mma16816(d[j], h0.x, h1.x, h0.y, h1.y, bv[j][s].x, bv[j][s].y, T());
-                            } else {
-                                const uint4 h0 = *reinterpret_cast<const uint4 *>(hp + 32 * s + 8 * q);
-                                const uint4 h1 = *reinterpret_cast<const uint4 *>(hp + 8 * kLd + 32 * s + 8 * q);
-    #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    mma16816(d[j], h0.x, h1.x, h0.y, h1.y, bv[j][s].x, bv[j][s].y, T());
-                                    mma16816(d[j], h0.z, h1.z, h0.w, h1.w, bv[j][s].z, bv[j][s].w, T());
-                                }
-                            }
+            }
+        }
+    };
+#pragma unroll
+    for (int s = 0; s < kAhead - 1; ++s) fetch(c0 + warp + s * kLoraWarps, s);
+    constexpr bool kNextB = NB == 2;  // more does not fit in registers
+    uint4 bv[4][kS], bn[4][kS];
+    if (kNextB) fetch_b(c0 + warp, bn);
+    ready();
+    int slot = 0;
+    for (int c = c0 + warp; c < c1; c += kLoraWarps) {
+        const int col = 32 * c + 8 * q;
+        if (kNextB) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int s = 0; s < kS; ++s) bv[j][s] = bn[j][s];
+            fetch_b(c + kLoraWarps, bn);
+        } else {
+            fetch_b(c, bv);
+        }
+        fetch(c + (kAhead - 1) * kLoraWarps, slot == 0 ? kAhead - 1 : slot - 1);
+        cp_async_wait<kAhead - 1>();
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            float d[4][4];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const uint16_t *hp = (z ? hl : hh) + (16 * i + g8) * kLd;
+#pragma unroll
+                for (int s = 0; s < kS; ++s) {
+                    if (NB == 2) {
+                        const uint2 h0 = *reinterpret_cast<const uint2 *>(hp + 4 * q);
+                        const uint2 h1 = *reinterpret_cast<const uint2 *>(hp + 8 * kLd + 4 * q);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (z == 0) mma16816_zero<T>(d[j], h0.x, h1.x, h0.y, h1.y, bv[j][s].x, bv[j][s].y);
+                            else mma16816(d[j], h0.x, h1.x, h0.y, h1.y, bv[j][s].x, bv[j][s].y, T());
                         }
-                    }
-    #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int32_t r = row_s[16 * i + 8 * h + g8];
-                        if (r >= 0 && col < p.n) {
-                            const float sc = scale_s[16 * i + 8 * h + g8];
-                            float f[8];
-                            Vec<T, 8>::unpack(old[i][h], f);
-    #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                f[2 * j] = fmaf(sc, d[j][2 * h], f[2 * j]);
-                                f[2 * j + 1] = fmaf(sc, d[j][2 * h + 1], f[2 * j + 1]);
-                            }
-                            *reinterpret_cast<uint4 *>(out + (int64_t)r * p.ldo + col) = Vec<T, 8>::pack(f);
+                    } else {
+                        const uint4 h0 = *reinterpret_cast<const uint4 *>(hp + 32 * s + 8 * q);
+                        const uint4 h1 = *reinterpret_cast<const uint4 *>(hp + 8 * kLd + 32 * s + 8 * q);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (z == 0 && s == 0) mma16816_zero<T>(d[j], h0.x, h1.x, h0.y, h1.y, bv[j][s].x, bv[j][s].y);
+                            else mma16816(d[j], h0.x, h1.x, h0.y, h1.y, bv[j][s].x, bv[j][s].y, T());
+                            mma16816(d[j], h0.z, h1.z, h0.w, h1.w, bv[j][s].z, bv[j][s].w, T());
                         }
                     }
                 }
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (row[i][h] >= 0 && col < p.n) {
+                    const float sc = scale_s[16 * i + 8 * h + g8];
+                    const uint64_t sc2 = pk2(sc, sc);
+                    uint64_t f[4];
+                    Vec<T, 8>::unpack2(base ? mine[((slot * MT + i) * 2 + h) * kLoraThreads] : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) f[j] = fma2(sc2, pk2(d[j][2 * h], d[j][2 * h + 1]), f[j]);
+                    *reinterpret_cast<uint4 *>(out + col + (int64_t)row[i][h] * p.ldo) = Vec<T, 8>::pack2(f);
+                }
+            }
+        }
+        slot = slot + 1 == kAhead ? 0 : slot + 1;
+    }
+    cp_async_wait<0>();
 }
 
-// Rows without a group: base (or zero), unless they are there already.
+// Rows without a group: base (or zero), unless they are there already; the
+// grid's first p.bare_ctas CTAs do it, a row per warp. Rows
+// without a group come in runs (a request's rows), so the warps take rows in
+// turn; a warp looks at 32 of its rows at a time.
 template <typename T>
 __device__ __forceinline__ void copy_bare_rows(const LoraParams &p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (p.base == p.out) return;
-    const int64_t warps = (int64_t)gridDim.x * kLoraWarps;
-    for (int64_t r = (int64_t)blockIdx.x * kLoraWarps + warp; r < p.m; r += warps) {
-        if (p.slots[r] >= 0) continue;
-        const T *src = static_cast<const T *>(p.base) + r * p.ldbase;
-        T *dst = static_cast<T *>(p.out) + r * p.ldo;
-        for (int c = 8 * lane; c < p.n; c += 256)
-            *reinterpret_cast<uint4 *>(dst + c) =
-                p.base ? *reinterpret_cast<const uint4 *>(src + c) : make_uint4(0, 0, 0, 0);
+    const int64_t warps = (int64_t)p.bare_ctas * kLoraWarps, me = (int64_t)blockIdx.x * kLoraWarps + warp;
+    for (int64_t i = 0; i * warps + me < p.m; i += 32) {
+        const int64_t look = (i + lane) * warps + me;
+        unsigned left = __ballot_sync(0xFFFFFFFFu, look < p.m && p.slots[look] < 0);
+        for (; left; left &= left - 1) {
+            const int64_t r = (i + __ffs((int)left) - 1) * warps + me;
+            const T *src = static_cast<const T *>(p.base) + r * p.ldbase;
+            T *dst = static_cast<T *>(p.out) + r * p.ldo;
+            for (int c0 = 8 * lane; c0 < p.n; c0 += 8 * 256) {  // 8 loads in flight
+                uint4 v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[j] = make_uint4(0, 0, 0, 0);
+                    if (p.base && c0 + 256 * j < p.n) v[j] = __ldg(reinterpret_cast<const uint4 *>(src + c0 + 256 * j));
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c0 + 256 * j < p.n) *reinterpret_cast<uint4 *>(dst + c0 + 256 * j) = v[j];
+            }
+        }
     }
+}
+
+// CTAs for that: none where the rows are in place, else a warp per row up to
+// one CTA per SM.
+static int bare_ctas(const LaunchCtx &ctx, const LoraParams &p) {
+    if (p.base == p.out) return 0;
+    const int64_t n = (p.m + kLoraWarps - 1) / kLoraWarps;
+    return (int)(n < ctx.num_sms ? n : ctx.num_sms);
 }
 
 // MT: 16-row blocks of a tile. NB: 8-column blocks of the padded rank.
@@ -217,7 +333,7 @@ template <typename T, int MT, int NB>
 struct LoraCfg {
     static constexpr int kRows = 16 * MT, kRank = 8 * NB;
     static constexpr int kLd = kRank + 8;   // row stride of the binary32 parts and of the 16-bit terms
-    static constexpr int kSmem = kLoraWarps * kRows * kLd * 4 + 2 * kRows * kLd * 2;
+    static constexpr int kSmem = kLoraWarps * kRows * kLd * 4 + 2 * kRows * kLd * 2 + kAheadBytes<MT>;
     static constexpr int kStep = NB >= 8 ? 1 : 2;  // steps of 32 elements of k in flight
 };
 
@@ -238,16 +354,17 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraParams p) 
     uint32_t csize;
     asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
     const uint32_t crank = cluster_ctarank();
-    const int cluster_id = (int)(blockIdx.x / csize);
+    if ((int)blockIdx.x < p.bare_ctas) {  // whole clusters
+        copy_bare_rows<T>(p);
+        return;
+    }
+    const int cluster_id = (int)((blockIdx.x - p.bare_ctas) / csize);
     const int tile = cluster_id / p.nsplit, part_n = cluster_id % p.nsplit;
 
-    for (int i = threadIdx.x; i <= p.groups; i += kLoraThreads) off[i] = p.offsets[i];
-    __syncthreads();
-    if (warp == 0) find_tile(off, p.groups, p.m, C::kRows, tile, tile_s);
-    __syncthreads();
+    cta_find_tile(p, off, C::kRows, tile, tile_s);
     const int group = tile_s[0], first = tile_s[1], count = tile_s[2];
     if (group == -2) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, kSiteBadOffsets);
+        if (threadIdx.x == 0) record_status(p.status, kSiteBadOffsets);
         return;
     }
     if (group >= 0) {
@@ -370,9 +487,10 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraParams p) 
         __syncthreads();
 
         const int64_t piece = (int64_t)part_n * csize + crank, pieces = (int64_t)p.nsplit * csize;
-        expand_tile<T, MT, NB>(p, group, row_s, scale_s, hh, hl, piece, pieces);
+        const int blocks = (p.n + 31) / 32;
+        expand_tile<T, MT, NB>(p, group, row_s, scale_s, hh, hl, smem + C::kSmem - kAheadBytes<MT>,
+                               (int)(blocks * piece / pieces), (int)(blocks * (piece + 1) / pieces), []() {});
     }
-    copy_bare_rows<T>(p);
     if (group >= 0 && csize > 1) cluster_sync();  // no CTA leaves while another reads its part
 }
 
@@ -380,16 +498,18 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraParams p) 
 // Many rows per adapter: two launches, h in the workspace.
 //
 // The first computes h = x A^T on the tensor cores of the fifth generation:
-// 128 rows of a group per tile, gathered from x four rows per copy, A's rows
+// 128 rows of a group per tile, gathered from x in 16-byte copies (a TMA gather
+// of four rows per copy measured 34 us against 24 for 8192 x 4096, rank 16), A's rows
 // beside them, k in steps of 64 through a ring of shared-memory stages, the
 // accumulator in tensor memory. The CTAs of a cluster split k and add their
 // parts through distributed shared memory; h leaves as its two 16-bit terms.
-// It is bound by reading x. The second is the fused form's second half on
-// tiles of 64 rows, bound by base and out. Two launches keep both streaming
+// It is bound by reading x. The second is the one-launch form's second
+// half on tiles of 32 rows, bound by base and out. Two launches keep both streaming
 // all the time; in one, a tile's reads of x and its writes alternate.
 constexpr int kShRows = 128;
 constexpr int kShK = 64;
-constexpr int kShThreads = 192;  // warps 0-3: accumulator; 4: copies; 5: products
+constexpr int kShThreads = 192;  // warps 0-3: copies of x, then the accumulator; 4: copies of A; 5: products
+constexpr int kShCopiers = 128;
 constexpr int kShX = kShRows * kShK * 2;
 
 template <int R>
@@ -407,7 +527,7 @@ SQ_HD int shrink_rank(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 :
 
 template <typename T, int R>
 __global__ void __launch_bounds__(kShThreads)
-    lora_shrink_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_a, const LoraParams p) {
+    lora_shrink_kernel(const __grid_constant__ CUtensorMap tm_a, const LoraParams p) {
     using C = ShrinkCfg<R>;
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], done;
@@ -417,59 +537,74 @@ __global__ void __launch_bounds__(kShThreads)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
     float *part = reinterpret_cast<float *>(dyn + (ring - smem_u32(dyn)));
-    griddep_wait();
-    griddep_launch();
-    uint32_t csize;
-    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
-    const uint32_t crank = cluster_ctarank();
-    for (int i = threadIdx.x; i <= p.groups; i += kShThreads) off[i] = p.offsets[i];
-    __syncthreads();
-    if (warp == 0) find_tile(off, p.groups, p.m, kShRows, (int)(blockIdx.x / csize), tile_s);
-    __syncthreads();
-    const int group = tile_s[0], first = tile_s[1], count = tile_s[2];
-    if (group < 0) {  // the same for the whole cluster
-        if (group == -2 && blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, kSiteBadOffsets);
-        return;
-    }
     if (warp == 5) {
         tmem_alloc(smem_u32(&tmem_s), C::kTmem);
         tmem_relinquish();
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&full[s]), kShCopiers + 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
         mbar_init(smem_u32(&done), 1);
         mbar_fence_init();
     }
     tc_fence_before();
-    __syncthreads();
+    griddep_wait();
+    griddep_launch();
+    uint32_t csize;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
+    const uint32_t crank = cluster_ctarank();
+    cta_find_tile(p, off, kShRows, (int)(blockIdx.x / csize), tile_s);  // its barrier also publishes the set-up above
     tc_fence_after();
+    const int group = tile_s[0], first = tile_s[1], count = tile_s[2];
+    if (group < 0) {  // the same for the whole cluster
+        if (warp == 5) tmem_dealloc(tmem_s, C::kTmem);
+        if (group == -2 && blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, kSiteBadOffsets);
+        return;
+    }
     const uint32_t tmem = tmem_s;
     const int blocks = (p.k + kShK - 1) / kShK;
     const int b0 = (int)((int64_t)blocks * crank / csize), b1 = (int)((int64_t)blocks * (crank + 1) / csize);
 
-    if (warp == 4) {
-        // Rows past the tile's end are not copied: what their lanes of the
-        // accumulator hold is not read.
-        const int quads = (count + 3) / 4;
-        int32_t r[4];
+    if (warp < 4) {
+        // 16-byte copies into the products' layout (128-byte rows, piece c of
+        // row r at c ^ (r % 8)): 8 threads per row, every 16th row. Rows past
+        // the tile's end are not copied: what their lanes of the accumulator
+        // hold is not read.
+        const int r0 = threadIdx.x >> 3, piece = threadIdx.x & 7;
+        const T *src[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int32_t v = p.rows[first + min(4 * lane + j, count - 1)];
-            r[j] = v >= 0 && v < p.m ? v : 0;  // reported, and left out, by the second launch
+        for (int j = 0; j < 8; ++j) {
+            src[j] = nullptr;
+            if (r0 + 16 * j < count) {
+                const int32_t v = p.rows[first + r0 + 16 * j];
+                // an invalid row is reported, and left out, by the second launch
+                src[j] = static_cast<const T *>(p.x) + (int64_t)(v >= 0 && v < p.m ? v : 0) * p.ldx + piece * 8;
+            }
         }
+        const uint32_t at = (uint32_t)(r0 * 128 + ((piece ^ (r0 & 7)) * 16));  // rows 16 apart: the same r % 8
         for (int b = b0; b < b1; ++b) {
             const int i = b - b0, s = i % C::kStages;
             const bool ok = mbar_wait_own(smem_u32(&empty[s]), ((i / C::kStages) & 1) ^ 1, p.status, kSiteLoraEmpty, p.wait_ns);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            const uint32_t dst = ring + s * C::kStage, bar = smem_u32(&full[s]);
-            if (lane == 0) mbar_arrive_expect_tx(bar, quads * 4 * kShK * 2 + R * kShK * 2);
-            __syncwarp();
-            if (lane < quads) tma_gather4(dst + lane * 4 * kShK * 2, &tm_x, b * kShK, r[0], r[1], r[2], r[3], bar);
-            if (lane == 0) tma_load_2d(dst + kShX, &tm_a, b * kShK, group * p.rank, bar);
+            const uint32_t dst = ring + s * C::kStage + at, in = b * kShK + piece * 8 < p.k ? 16u : 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (src[j]) cp_async16_zfill(dst + j * 16 * 128, in ? src[j] + b * kShK : src[j], in);
+            cp_async_arrive(smem_u32(&full[s]));
         }
+    } else if (warp == 4) {
+        if (lane == 0) {
+            for (int b = b0; b < b1; ++b) {
+                const int i = b - b0, s = i % C::kStages;
+                if (!mbar_wait_own(smem_u32(&empty[s]), ((i / C::kStages) & 1) ^ 1, p.status, kSiteLoraEmpty, p.wait_ns)) break;
+                const uint32_t bar = smem_u32(&full[s]);
+                mbar_arrive_expect_tx(bar, R * kShK * 2);
+                tma_load_2d(ring + s * C::kStage + kShX, &tm_a, b * kShK, group * p.rank, bar);
+            }
+        }
+        __syncwarp();
     } else if (warp == 5) {
         if (lane == 0) {
             // D binary32; A and B of type T, both K-major; N = R, M = 128
@@ -478,6 +613,7 @@ __global__ void __launch_bounds__(kShThreads)
             for (int b = b0; b < b1; ++b) {
                 const int i = b - b0, s = i % C::kStages;
                 if (!mbar_wait_own(smem_u32(&full[s]), (i / C::kStages) & 1, p.status, kSiteLoraFull, p.wait_ns)) break;
+                fence_proxy_async();  // x came through the generic proxy
                 tc_fence_after();
                 const uint32_t st = ring + s * C::kStage;
                 const uint64_t dx = smem_desc(st, 16, 8 * kShK * 2, 2u), da = smem_desc(st + kShX, 16, 8 * kShK * 2, 2u);
@@ -557,26 +693,50 @@ __global__ void __launch_bounds__(kShThreads)
     cluster_sync();  // no CTA leaves while another reads its part
 }
 
-constexpr int kExRows = 64;
+// Tiles of 32 rows: 64 rows halve what is read of B (from L2) but leave two
+// CTAs of registers on an SM; 8192 x 4096, rank 16: 33.6 us against 30.0, 4099
+// x 4096, rank 64, 64 adapters: 40.2 against 33.5. More CTAs than these take
+// the L1 that B's lines need: with four, 32.5 and 35.8 us.
+constexpr int kExRows = 32;
+template <int NB>
+constexpr int kExPerSm = NB <= 4 ? 3 : 2;
 
+
+// The tiles' blocks of 32 columns, laid end to end, are divided evenly among
+// the CTAs, which stay for the whole launch: a CTA's share ends inside a tile.
 template <typename T, int NB>
-__global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraParams p) {
+__global__ void __launch_bounds__(kLoraThreads, kExPerSm<NB>) lora_expand_kernel(const LoraParams p) {
     constexpr int R = 8 * NB, kLd = R + 8;
+    extern __shared__ __align__(16) uint8_t ahead[];
     __shared__ __align__(16) uint16_t hh[kExRows * kLd], hl[kExRows * kLd];
-    __shared__ int32_t off[kGroupsMax + 1];
-    __shared__ int32_t tile_s[3];
+    __shared__ int32_t off[kGroupsMax + 1], tiles[kGroupsMax + 1];
     __shared__ int32_t row_s[kExRows];
     __shared__ float scale_s[kExRows];
-    griddep_wait();
-    griddep_launch();
-    const int warp = threadIdx.x >> 5;
+    // This launch starts when every CTA of the first has passed its own wait,
+    // so all that came before the first (routing, base, weights) is there;
+    // only h and its scales, the first launch's results, need the wait below.
+    if (p.base != p.out) copy_bare_rows<T>(p);
     for (int i = threadIdx.x; i <= p.groups; i += kLoraThreads) off[i] = p.offsets[i];
     __syncthreads();
-    if (warp == 0) find_tile(off, p.groups, p.m, kExRows, (int)(blockIdx.x / p.nsplit), tile_s);
+    __shared__ int table_ok;
+    if (threadIdx.x < 32) {
+        const bool ok = build_tiles(off, p.groups, p.m, kExRows, tiles);
+        if (threadIdx.x == 0) table_ok = ok;
+    }
     __syncthreads();
-    const int group = tile_s[0], first = tile_s[1], count = tile_s[2];
-    if (group == -2) return;  // reported by the first launch
-    if (group >= 0) {
+    if (!table_ok) {  // reported by the first launch
+        griddep_wait();
+        return;
+    }
+    const int blocks = (p.n + 31) / 32;
+    const int64_t work = (int64_t)tiles[p.groups] * blocks, ctas = gridDim.x, me = blockIdx.x;
+    const int64_t w1 = work * (me + 1) / ctas;
+    bool waited = false;
+    for (int64_t w = work * me / ctas; w < w1;) {
+        const int tile = (int)(w / blocks), c0 = (int)(w % blocks), c1 = (int)min((int64_t)blocks, c0 + w1 - w);
+        const int group = group_of_tile(tiles, p.groups, tile);
+        const int first = off[group] + (tile - tiles[group]) * kExRows, count = min(kExRows, off[group + 1] - first);
+        __syncthreads();  // the last tile's rows and h are no longer needed
         if (threadIdx.x < kExRows) {
             int32_t r = -1;
             if ((int)threadIdx.x < count) {
@@ -585,21 +745,27 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraPar
                     record_status(p.status, kSiteBadRowIndex);
                     r = -1;
                 }
-                scale_s[threadIdx.x] = (p.scales ? p.scales[group] : 1.0f) * p.hscale[first + threadIdx.x];
             }
             row_s[threadIdx.x] = r;
         }
-        const uint4 *h = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.h) + (int64_t)first * 2 * R);
-        for (int i = threadIdx.x; i < kExRows * R / 4; i += kLoraThreads) {
-            const int row = i / (R / 4), c = i % (R / 4);  // 16-byte pieces: R / 8 of each term
-            const uint4 v = row < count ? h[i] : make_uint4(0, 0, 0, 0);
-            uint16_t *dst = c < R / 8 ? hh + row * kLd + 8 * c : hl + row * kLd + 8 * (c - R / 8);
-            *reinterpret_cast<uint4 *>(dst) = v;
-        }
         __syncthreads();
-        expand_tile<T, kExRows / 16, NB>(p, group, row_s, scale_s, hh, hl, blockIdx.x % p.nsplit, p.nsplit);
+        expand_tile<T, kExRows / 16, NB>(p, group, row_s, scale_s, hh, hl, ahead, c0, c1, [&]() {
+            if (!waited) griddep_wait();
+            waited = true;
+            if ((int)threadIdx.x < count)
+                scale_s[threadIdx.x] = (p.scales ? p.scales[group] : 1.0f) * __ldcg(p.hscale + first + threadIdx.x);
+            const uint4 *h = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.h) + (int64_t)first * 2 * R);
+            for (int i = threadIdx.x; i < kExRows * R / 4; i += kLoraThreads) {
+                const int row = i / (R / 4), c = i % (R / 4);  // 16-byte pieces: R / 8 of each term
+                const uint4 v = row < count ? __ldcg(h + i) : make_uint4(0, 0, 0, 0);
+                uint16_t *dst = c < R / 8 ? hh + row * kLd + 8 * c : hl + row * kLd + 8 * (c - R / 8);
+                *reinterpret_cast<uint4 *>(dst) = v;
+            }
+            __syncthreads();
+        });
+        w += c1 - c0;
     }
-    copy_bare_rows<T>(p);
+    if (!waited) griddep_wait();
 }
 
 // Tiles of `rows` rows: a bound on sum ceil(rows of a group / rows).
@@ -612,20 +778,24 @@ template <typename T, int NB>
 static sharq_status lora_two(LaunchCtx &ctx, LoraParams p) {
     constexpr int R = 8 * NB;
     using C = ShrinkCfg<R>;
-    CUtensorMap tm_x, tm_a;
-    if (!make_row_map(&tm_x, p.x, (uint64_t)p.k, (uint64_t)p.m, (uint64_t)p.ldx * 2, 1) ||
-        !make_row_map(&tm_a, p.a, (uint64_t)p.k, (uint64_t)p.groups * p.rank, (uint64_t)p.k * 2, R))
+    CUtensorMap tm_a;
+    if (!make_row_map(&tm_a, p.a, (uint64_t)p.k, (uint64_t)p.groups * p.rank, (uint64_t)p.k * 2, R))
         return SHARQ_ERR_CUDA;
     SQ_SMEM_ONCE((lora_shrink_kernel<T, R>), C::kSmem);
     const int64_t tiles = tiles_bound(p, kShRows);
+    // Splits of k: until the tiles would take more than 3 CTAs per SM (two fit;
+    // the bound on the tiles is rarely met)
     int cluster = 1;
-    while (cluster < 8 && tiles * cluster < 2 * ctx.num_sms && p.k >= 2 * kShK * cluster) cluster *= 2;
-    sharq_status st = launch_pdl(ctx, lora_shrink_kernel<T, R>, tiles * cluster, kShThreads, C::kSmem, cluster, tm_x, tm_a, p);
+    while (cluster < 8 && tiles * cluster * 2 <= 3 * ctx.num_sms && p.k >= 2 * kShK * cluster) cluster *= 2;
+    sharq_status st = launch_pdl(ctx, lora_shrink_kernel<T, R>, tiles * cluster, kShThreads, C::kSmem, cluster, tm_a, p);
     if (st != SHARQ_OK) return st;
-    const int64_t ex = tiles_bound(p, kExRows);
-    p.nsplit = 1;
-    while (p.nsplit < 32 && ex * p.nsplit < 4 * ctx.num_sms && p.n >= 512 * p.nsplit) p.nsplit *= 2;
-    return launch_pdl(ctx, lora_expand_kernel<T, NB>, ex * p.nsplit, kLoraThreads, 0, 1, p);
+    // CTAs that stay, unless that leaves a warp less than a block
+    const int64_t ex = tiles_bound(p, kExRows) * ((p.n + 32 * kLoraWarps - 1) / (32 * kLoraWarps));
+    const int64_t stay = (int64_t)kExPerSm<NB> * ctx.num_sms;
+    const int64_t ctas = ex < stay ? ex : stay;
+    p.bare_ctas = (int32_t)ctas;
+    SQ_SMEM_ONCE((lora_expand_kernel<T, NB>), kAheadBytes<kExRows / 16>);
+    return launch_pdl(ctx, lora_expand_kernel<T, NB>, ctas, kLoraThreads, kAheadBytes<kExRows / 16>, 1, p);
 }
 
 // Whether a call takes the two-launch form (and so needs a workspace): rows
@@ -648,7 +818,8 @@ static sharq_status lora_run(LaunchCtx &ctx, LoraParams p) {
     while (cluster < 8 && tiles * cluster < 2 * ctx.num_sms && p.k >= 512 * cluster) cluster *= 2;
     p.nsplit = 1;
     while (p.nsplit < 16 && tiles * cluster * p.nsplit < ctx.num_sms && p.n >= 512 * cluster * p.nsplit) p.nsplit *= 2;
-    return launch_pdl(ctx, lora_kernel<T, MT, NB>, tiles * cluster * p.nsplit, kLoraThreads, C::kSmem, cluster, p);
+    p.bare_ctas = (int32_t)round_up(bare_ctas(ctx, p), cluster);
+    return launch_pdl(ctx, lora_kernel<T, MT, NB>, p.bare_ctas + tiles * cluster * p.nsplit, kLoraThreads, C::kSmem, cluster, p);
 }
 
 template <typename T>
@@ -672,8 +843,8 @@ sharq_status launch_lora(LaunchCtx &ctx, const void *x, int64_t ldx, int64_t m, 
                          const int32_t *rows, const int32_t *slots, int dtype, const void *base, int64_t ldbase, void *out,
                          int64_t ldo, void *ws) {
     if (m == 0) return SHARQ_OK;
-    LoraParams p{x, a, b, base, scales, out, offsets, rows, slots, ldx, ldbase, ldo, m,
-                 (int32_t)k, (int32_t)n, (int32_t)rank, (int32_t)groups, 1, ctx.status, ctx.wait_ns, ws,
+    LoraParams p{x, a, b, base, scales, out, offsets, rows, slots, (int32_t)ldx, (int32_t)ldbase, (int32_t)ldo, m,
+                 (int32_t)k, (int32_t)n, (int32_t)rank, (int32_t)groups, 1, 0, ctx.status, ctx.wait_ns, ws,
                  reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + round_up(m * 4 * shrink_rank(rank), kAlign))};
     return dtype == SHARQ_F16 ? lora_any<__half>(ctx, p) : lora_any<__nv_bfloat16>(ctx, p);
 }

@@ -9,7 +9,17 @@ import pytest
 import torch
 
 import sparsity_gemm_b200 as sq
-from test_binding_checks import _as_cuda
+from test_binding_checks import _AsCuda
+
+
+class _OnCuda(_AsCuda):
+    def get_device(self):
+        return 0
+
+
+def _as_cuda(t):
+    return t.as_subclass(_OnCuda)
+
 
 P = lambda i, off=0: C.c_void_p((i << 32) + off)  # noqa: E731  far apart, aligned, never dereferenced
 BIG = 1 << 30
@@ -121,10 +131,15 @@ def here(monkeypatch):
     for name in ("layer_norm", "layer_norm_backward", "route", "permute_rows", "combine", "combine_backward", "lora"):
         getattr(fake, "sharq_" + name).return_value = sq.OK
     monkeypatch.setattr(sq, "lib", lambda: fake)
-    monkeypatch.setattr(sq, "_empty", lambda shape, dtype, device, stream: _as_cuda(torch.zeros(shape, dtype=dtype)))
+    monkeypatch.setattr(sq, "_new", lambda like, shape, dtype, stream: _as_cuda(torch.zeros(shape, dtype=dtype)))
+    monkeypatch.setattr(sq, "_new_like", lambda t, stream: _as_cuda(torch.zeros(t.shape, dtype=t.dtype)))
+    monkeypatch.setattr(sq, "_raw", lambda stream, dev: 0)
+    sq._lora_bytes.cache_clear()
+    sq._norm_backward_bytes.cache_clear()
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: mock.Mock(cuda_stream=0))
-    return fake
+    yield fake
+    sq._lora_bytes.cache_clear()
+    sq._norm_backward_bytes.cache_clear()
 
 
 def _routing(m=6, top_k=2, groups=3):
