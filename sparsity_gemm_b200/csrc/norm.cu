@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(const NormP
 // in their order. The next row is loaded before the current one is reduced.
 constexpr int kBwdCols = 16;          // columns per thread
 constexpr int kBwdThreads = 512;      // most threads of a CTA
+constexpr int kBwdSmall = 256;        // threads up to which an SM holds more than one
 constexpr int kBwdCluster = 8;        // most CTAs of a row
 constexpr int kBwdWarps = 8;          // rows at a time in a CTA of the warp form
 
@@ -401,23 +402,15 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
 // with its part of the columns) per row, kBwdCols columns per thread, and a
 // ring of rows of x and dy filled by bulk copies several rows ahead. The
 // barrier of a row's reduction also frees its ring slot.
-#ifndef BWD_OCC
-#define BWD_OCC 2
-#endif
 constexpr int kRingMax = 8;            // most rows in a ring
 constexpr int kRingBytes = 160 << 10;  // shared memory of an SM's rings
 
-#ifndef RCOLS
-#define RCOLS 16
-#endif
-#ifndef RMAXT
-#define RMAXT 256
-#endif
-template <typename T, int VW, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= RMAXT ? BWD_OCC : 1)
+// FULL: every thread has all its columns.
+template <typename T, int VW, int MAXT, bool FULL>
+__global__ void __launch_bounds__(MAXT, MAXT <= kBwdSmall ? 2 : 1)
     norm_bwd_ring_kernel(const NormBwdParams p, int stages, uint64_t wait_ns, unsigned *status) {
     using V = Vec<T, VW>;
-    constexpr int NV = RCOLS / VW, H = VW / 2;
+    constexpr int NV = kBwdCols / VW, H = VW / 2;
     extern __shared__ __align__(128) uint8_t ring[];  // [stages][x, dy][part of a row]
     __shared__ uint64_t full[kRingMax];
     __shared__ __align__(16) float2 red[2][MAXT / 32];
@@ -455,15 +448,16 @@ __global__ void __launch_bounds__(MAXT, MAXT <= RMAXT ? BWD_OCC : 1)
     if (tid == 0)
         for (int it = 0; it < stages && it < iters; ++it) issue(it, it);
     const float inv_k = 1.0f / (float)p.k;
-    typename V::P wv[NV];
-    uint64_t dw[NV][H], db[NV][H];
+    uint64_t wf[NV][H], dw[NV][H], db[NV][H];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = i * threads + tid;
-        wv[i] = wp && c < cnt ? V::load(wp + (int64_t)(v0 + c) * VW) : V::ones();
+        V::unpack2(wp && (FULL || c < cnt) ? V::load(wp + (int64_t)(v0 + c) * VW) : V::ones(), wf[i]);
 #pragma unroll
         for (int e = 0; e < H; ++e) dw[i][e] = db[i][e] = 0;
     }
+    T *dx_row = dxp + part * p.k + tid * VW;
+    const int64_t dx_step = parts * p.k;
     float mu_n = p.rms || iters <= 0 ? 0.0f : p.mean[part], rs_n = iters <= 0 ? 0.0f : p.rstd[part];
     int slot = 0;
     uint32_t phase = 0;
@@ -481,17 +475,16 @@ __global__ void __launch_bounds__(MAXT, MAXT <= RMAXT ? BWD_OCC : 1)
         for (int i = 0; i < NV; ++i) {
             const int c = i * threads + tid;
             const uint8_t *at = ring + slot * 2 * stride + c * 16;
-            uint64_t df[H], wf[H];
+            uint64_t df[H];
             // columns past the row: dy = 0, so they add nothing
-            V::unpack2(c < cnt ? *reinterpret_cast<const typename V::P *>(at) : V::zero(), h[i]);
-            V::unpack2(c < cnt ? *reinterpret_cast<const typename V::P *>(at + stride) : V::zero(), df);
-            V::unpack2(wv[i], wf);
+            V::unpack2(FULL || c < cnt ? *reinterpret_cast<const typename V::P *>(at) : V::zero(), h[i]);
+            V::unpack2(FULL || c < cnt ? *reinterpret_cast<const typename V::P *>(at + stride) : V::zero(), df);
 #pragma unroll
             for (int e = 0; e < H; ++e) {
                 h[i][e] = mul2(add2(h[i][e], mu2), rs2);
                 dw[i][e] = fma2(df[e], h[i][e], dw[i][e]);
                 db[i][e] = add2(db[i][e], df[e]);
-                g[i][e] = mul2(df[e], wf[e]);
+                g[i][e] = mul2(df[e], wf[i][e]);
                 t1 = add2(t1, g[i][e]);
                 t2 = fma2(g[i][e], h[i][e], t2);
             }
@@ -535,8 +528,9 @@ __global__ void __launch_bounds__(MAXT, MAXT <= RMAXT ? BWD_OCC : 1)
             const int c = i * threads + tid;
 #pragma unroll
             for (int e = 0; e < H; ++e) g[i][e] = fma2(fma2(h[i][e], m2n, g[i][e]), rs2, m1n);
-            if (c < cnt) V::store(dxp + row * p.k + (int64_t)c * VW, V::pack2(g[i]));
+            if (FULL || c < cnt) V::store(dx_row + (int64_t)i * threads * VW, V::pack2(g[i]));
         }
+        dx_row += dx_step;
         if (++slot == stages) {
             slot = 0;
             phase ^= 1;
@@ -616,11 +610,11 @@ static int bwd_cluster(int64_t k) {
     return c;
 }
 static int bwd_threads(int64_t k, int cluster) {
-    return (int)round_up(((k + RCOLS - 1) / RCOLS + cluster - 1) / cluster, 32);
+    return (int)round_up(((k + kBwdCols - 1) / kBwdCols + cluster - 1) / cluster, 32);
 }
 static int bwd_per_sm(int threads) {
-    if (threads > RMAXT) return 1;
-    const int n = BWD_OCC * RMAXT / threads;
+    if (threads > kBwdSmall) return 1;
+    const int n = 2 * kBwdSmall / threads;
     return n > 8 ? 8 : n;
 }
 
@@ -651,14 +645,18 @@ static sharq_status norm_bwd(LaunchCtx &ctx, const NormBwdParams &p) {
         const int64_t pair = 2 * 16 * ((p.k / VW + cluster - 1) / cluster);
         const int64_t fit = kRingBytes / bwd_per_sm(threads) / pair;
         const int stages = fit > kRingMax ? kRingMax : (int)fit;  // at least 2: a pair of rows has at most 64 KB
-        if (threads <= RMAXT) {
-            SQ_SMEM_ONCE((norm_bwd_ring_kernel<T, VW, RMAXT>), kRingBytes);
-            return launch_pdl(ctx, norm_bwd_ring_kernel<T, VW, RMAXT>, (int64_t)p.parts * cluster, threads,
-                              (size_t)(stages * pair), cluster, p, stages, ctx.wait_ns, ctx.status);
-        }
-        SQ_SMEM_ONCE((norm_bwd_ring_kernel<T, VW, 1024 * 8 / RCOLS>), kRingBytes);
-        return launch_pdl(ctx, norm_bwd_ring_kernel<T, VW, 1024 * 8 / RCOLS>, (int64_t)p.parts * cluster, threads,
-                          (size_t)(stages * pair), cluster, p, stages, ctx.wait_ns, ctx.status);
+        const bool full = p.k % ((int64_t)cluster * threads * kBwdCols) == 0;
+        auto run = [&](auto kernel) {
+            return launch_pdl(ctx, kernel, (int64_t)p.parts * cluster, threads, (size_t)(stages * pair), cluster, p, stages,
+                              ctx.wait_ns, ctx.status);
+        };
+        SQ_SMEM_ONCE((norm_bwd_ring_kernel<T, VW, kBwdSmall, true>), kRingBytes);
+        SQ_SMEM_ONCE((norm_bwd_ring_kernel<T, VW, kBwdSmall, false>), kRingBytes);
+        SQ_SMEM_ONCE((norm_bwd_ring_kernel<T, VW, kBwdThreads, true>), kRingBytes);
+        SQ_SMEM_ONCE((norm_bwd_ring_kernel<T, VW, kBwdThreads, false>), kRingBytes);
+        if (threads <= kBwdSmall)
+            return full ? run(norm_bwd_ring_kernel<T, VW, kBwdSmall, true>) : run(norm_bwd_ring_kernel<T, VW, kBwdSmall, false>);
+        return full ? run(norm_bwd_ring_kernel<T, VW, kBwdThreads, true>) : run(norm_bwd_ring_kernel<T, VW, kBwdThreads, false>);
     } else {
         return launch_pdl(ctx, norm_bwd_kernel<T, VW, false>, (int64_t)p.parts * cluster, threads, 0, cluster, p);
     }

@@ -22,14 +22,16 @@ namespace sq {
 // ---------------------------------------------------------------------------
 // Route: one launch of one cluster. Every warp owns a contiguous run of
 // entries, so the sort is stable if a warp's entries of a group follow those
-// of the warps before it. Each warp counts its entries per group (lanes with
-// the same group meet in a match, one lane adds), a scan over warps, CTAs
-// (through distributed shared memory) and groups turns the counts into first
-// slots, and a second walk over the entries hands the slots out.
+// of the warps before it. Each warp counts its entries per group (the lanes
+// with the same group find each other, one adds), which also gives each entry
+// its place among its warp's entries of the group; a scan over warps, CTAs
+// (through distributed shared memory) and groups gives the rest of its slot.
+// Bound by latency (launch, cluster barriers, one load and one store): 32768
+// entries of 128 groups move 0.4 MB.
 constexpr int kRouteThreads = 1024;
-constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kRouteFew = 256;     // threads where entries and groups are few
 constexpr int kRouteCluster = 8;
-constexpr int kRouteKeep = 4;  // steps of 32 entries whose groups a lane keeps in registers
+constexpr int kRouteKeep = 4;      // steps of 32 entries whose groups and places a lane keeps in registers
 
 struct RouteParams {
     const void *ids;
@@ -38,68 +40,110 @@ struct RouteParams {
     int32_t *offsets, *rows, *slots;
 };
 
-template <typename ID>
+// Counts per group of a warp in shared memory: an odd row stride spreads the
+// 8 x 4 reads of the scan over all banks.
+__host__ __device__ __forceinline__ int route_stride(int groups) { return groups | 1; }
+
+// The lanes with my value (below 2^bits): a ballot per bit. A match
+// instruction does the same, but one SM gets through about one in 120 cycles
+// (32768 entries: 12 us with it, 10 us like this).
+__device__ __forceinline__ unsigned peers_of(int32_t v, int bits) {
+    unsigned peers = 0xFFFFFFFFu;
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (v >> b) & 1;
+        const unsigned with = __ballot_sync(0xFFFFFFFFu, one);
+        peers &= one ? with : ~with;
+    }
+    return peers;
+}
+
+// LONG: runs of more than kRouteKeep * 32 entries; a second walk over them
+// then hands the slots out.
+template <typename ID, bool LONG>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams p) {
     extern __shared__ int32_t sm[];
-    int32_t *hist = sm;                               // [kRouteWarps][groups]
-    int32_t *mine = sm + kRouteWarps * p.groups;      // [groups] entries of this CTA
-    __shared__ int32_t scan[kRouteWarps];
-    __shared__ int32_t total_s;
+    __shared__ int32_t scan[32];
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = threadIdx.x;
+    const int stride = route_stride(p.groups), bits = 32 - __clz(p.groups);
+    int32_t *hist = sm;                        // [warps][stride]
+    int32_t *mine = sm + warps * stride;       // [groups] entries of this CTA
+    int32_t *base = mine + p.groups;           // [groups] first slot of this CTA's entries
+    for (int i = threadIdx.x; i < warps * stride; i += blockDim.x) hist[i] = 0;
     griddep_wait();
     griddep_launch();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = threadIdx.x;
     const uint32_t rank = cluster_ctarank();
-    const int64_t ctas = gridDim.x;
-    const int64_t run = ((p.entries + ctas * kRouteWarps - 1) / (ctas * kRouteWarps) + 31) / 32 * 32;
-    const int64_t e0 = ((int64_t)rank * kRouteWarps + warp) * run;
-    const int64_t e1 = min(e0 + run, p.entries);
+    const int ctas = (int)gridDim.x;
+    // at most 2^30 entries: 32-bit arithmetic
+    const uint32_t run = (((uint32_t)p.entries + ctas * warps - 1) / (uint32_t)(ctas * warps) + 31) / 32 * 32;
+    const int32_t e0 = (int32_t)min((int64_t)(rank * warps + warp) * run, p.entries);
+    const int32_t e1 = (int32_t)min((int64_t)e0 + run, p.entries);
     const ID *ids = static_cast<const ID *>(p.ids);
-    int32_t *wh = hist + warp * p.groups;
+    int32_t *wh = hist + warp * stride;
 
-    for (int i = threadIdx.x; i < kRouteWarps * p.groups; i += kRouteThreads) hist[i] = 0;
-    auto group_at = [&](int64_t e) -> int32_t {
+    auto group_at = [&](int32_t e) -> int32_t {
         if (e >= e1) return -1;
         const ID v = ids[e];
         return v >= 0 && v < (ID)p.groups ? (int32_t)v : -1;
     };
-    int32_t kept[kRouteKeep];
+    // The entry's place among the warp's entries of its group so far; adds
+    // the step's entries to the counts in wh.
+    auto count = [&](int32_t v) -> int32_t {
+        const unsigned peers = peers_of(v < 0 ? p.groups : v, bits);
+        const int32_t before = v >= 0 ? wh[v] : 0;
+        __syncwarp();
+        if (v >= 0 && lane == __ffs((int)peers) - 1) wh[v] = before + __popc(peers);
+        __syncwarp();
+        return before + __popc(peers & ((1u << lane) - 1u));
+    };
+    int32_t kept[kRouteKeep], place[kRouteKeep];
 #pragma unroll
     for (int s = 0; s < kRouteKeep; ++s) kept[s] = group_at(e0 + s * 32 + lane);
     __syncthreads();
-
-    // The lanes of my group before me in a step, and whether I add for them.
-    auto count = [&](int32_t v) {
-        const unsigned peers = __match_any_sync(0xFFFFFFFFu, v);
-        if (v >= 0 && lane == __ffs((int)peers) - 1) wh[v] += __popc(peers);
-        __syncwarp();
-    };
 #pragma unroll
-    for (int s = 0; s < kRouteKeep; ++s)
-        if (e0 + s * 32 < e1) count(kept[s]);
-    for (int64_t e = e0 + kRouteKeep * 32; e < e1; e += 32) count(group_at(e + lane));
+    for (int s = 0; s < kRouteKeep; ++s) place[s] = e0 + s * 32 < e1 ? count(kept[s]) : 0;
+    if (LONG)
+        for (int32_t e = e0 + kRouteKeep * 32; e < e1; e += 32) count(group_at(e + lane));
     __syncthreads();
 
-    if (g < p.groups) {
-        int32_t run_sum = 0;
-#pragma unroll 8
-        for (int w = 0; w < kRouteWarps; ++w) {
-            const int32_t c = hist[w * p.groups + g];
-            hist[w * p.groups + g] = run_sum;
-            run_sum += c;
+    // scan over the warps: 8 lanes per group, 4 warps each
+    const int sub = threadIdx.x & 7;
+    for (int h = threadIdx.x >> 3; h < (p.groups + 3) / 4 * 4; h += blockDim.x >> 3) {  // 4 groups of a warp together
+        int32_t c[4], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[i] = h < p.groups && 4 * sub + i < warps ? hist[(4 * sub + i) * stride + h] : 0;
+            sum += c[i];
         }
-        mine[g] = run_sum;
+        int32_t inc = sum;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+            const int32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o, 8);
+            if (sub >= o) inc += v;
+        }
+        int32_t at = inc - sum;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (h < p.groups && 4 * sub + i < warps) hist[(4 * sub + i) * stride + h] = at;
+            at += c[i];
+        }
+        if (sub == 7 && h < p.groups) mine[h] = inc;
     }
     int32_t before = 0, all = 0;
     if (ctas > 1) {
         cluster_sync();
-        if (g < p.groups)
-            for (uint32_t c = 0; c < (uint32_t)ctas; ++c) {
-                const int32_t v = (int32_t)ld_cluster_u32(mapa_shared(smem_u32(mine + g), c));
-                if (c < rank) before += v;
+        if (g < p.groups) {
+            const uint32_t at = smem_u32(mine + g);
+#pragma unroll
+            for (int c = 0; c < kRouteCluster; ++c) {
+                const int32_t v = c < ctas ? (int32_t)ld_cluster_u32(mapa_shared(at, (uint32_t)c)) : 0;
+                if (c < (int)rank) before += v;
                 all += v;
             }
-    } else if (g < p.groups) {
-        all = mine[g];
+        }
+        cluster_arrive_relaxed();  // this thread reads no other CTA's counts any more
+    } else {
+        __syncthreads();
+        if (g < p.groups) all = mine[g];
     }
     // exclusive scan of the groups' totals over the CTA's threads
     int32_t inc = all;
@@ -110,64 +154,72 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
     }
     if (lane == 31) scan[warp] = inc;
     __syncthreads();
-    if (warp == 0) {
-        int32_t v = scan[lane];
+    int32_t v = lane < warps ? scan[lane] : 0;  // every warp scans the warps' totals for itself
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-            if (lane >= o) v += u;
-        }
-        scan[lane] = v;
-        if (lane == 31) total_s = v;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += u;
     }
-    __syncthreads();
-    const int32_t first = inc - all + (warp > 0 ? scan[warp - 1] : 0);
-    const int32_t total = total_s;
+    const int32_t total = __shfl_sync(0xFFFFFFFFu, v, 31);
+    const int32_t ahead = __shfl_sync(0xFFFFFFFFu, v, warp > 0 ? warp - 1 : 0);
+    const int32_t first = inc - all + (warp > 0 ? ahead : 0);
     if (g < p.groups) {
         if (rank == 0) {
             p.offsets[g] = first;
             if (g == p.groups - 1) p.offsets[p.groups] = total;
         }
-#pragma unroll 8
-        for (int w = 0; w < kRouteWarps; ++w) hist[w * p.groups + g] += first + before;
+        base[g] = first + before;
     }
     __syncthreads();
 
-    auto place = [&](int32_t v, int64_t e) {
-        const unsigned peers = __match_any_sync(0xFFFFFFFFu, v);
-        int32_t slot = -1;
-        if (v >= 0) slot = wh[v] + __popc(peers & ((1u << lane) - 1u));
-        __syncwarp();
-        if (v >= 0 && lane == __ffs((int)peers) - 1) wh[v] += __popc(peers);
-        __syncwarp();
+    auto put = [&](int32_t v, int32_t e, int32_t slot) {
         if (e < e1) {
-            p.slots[e] = slot;
-            if (slot >= 0) p.rows[slot] = (int32_t)(e / p.top_k);
+            p.slots[e] = v >= 0 ? slot : -1;
+            if (v >= 0) p.rows[slot] = (int32_t)((uint32_t)e / (uint32_t)p.top_k);
         }
     };
 #pragma unroll
     for (int s = 0; s < kRouteKeep; ++s)
-        if (e0 + s * 32 < e1) place(kept[s], e0 + s * 32 + lane);
-    for (int64_t e = e0 + kRouteKeep * 32; e < e1; e += 32) place(group_at(e + lane), e + lane);
+        if (e0 + s * 32 < e1)
+            put(kept[s], e0 + s * 32 + lane, kept[s] >= 0 ? base[kept[s]] + wh[kept[s]] + place[s] : 0);
+    if (LONG && e0 < e1) {
+        // the kept entries' part of the counts comes first
+        __syncwarp();
+#pragma unroll
+        for (int s = 0; s < kRouteKeep; ++s)
+            if (e0 + s * 32 < e1) count(kept[s]);
+        for (int32_t e = e0 + kRouteKeep * 32; e < e1; e += 32) {
+            const int32_t v = group_at(e + lane);
+            const int32_t at = count(v);
+            put(v, e + lane, v >= 0 ? base[v] + at : 0);
+        }
+    }
     // rows behind the last group's
-    for (int64_t i = total + (int64_t)rank * kRouteThreads + threadIdx.x; i < p.entries; i += ctas * kRouteThreads)
+    for (int64_t i = total + (int64_t)rank * blockDim.x + threadIdx.x; i < p.entries; i += (int64_t)ctas * blockDim.x)
         p.rows[i] = -1;
-    if (ctas > 1) cluster_sync();  // no CTA leaves while another reads its counts
+    if (ctas > 1) cluster_wait();  // no CTA leaves while another reads its counts
+}
+
+template <typename ID, bool LONG>
+static sharq_status route_run(LaunchCtx &ctx, const RouteParams &p, int ctas, int threads) {
+    auto bytes = [](int warps, int groups) { return (size_t)(warps * route_stride(groups) + 2 * groups) * sizeof(int32_t); };
+    SQ_SMEM_ONCE((route_kernel<ID, LONG>), bytes(kRouteThreads / 32, (int)kGroupsMax));
+    return launch_pdl(ctx, route_kernel<ID, LONG>, ctas, threads, bytes(threads / 32, p.groups), ctas, p);
 }
 
 template <typename ID>
-static sharq_status route_run(LaunchCtx &ctx, const RouteParams &p) {
-    const size_t smem = (size_t)(kRouteWarps + 1) * p.groups * sizeof(int32_t);
-    SQ_SMEM_ONCE(route_kernel<ID>, (kRouteWarps + 1) * kGroupsMax * sizeof(int32_t));
+static sharq_status route_any(LaunchCtx &ctx, const RouteParams &p) {
+    const int threads = p.entries <= 4 * kRouteFew && p.groups <= kRouteFew ? kRouteFew : kRouteThreads;
     int ctas = 1;
-    while (ctas < kRouteCluster && p.entries > (int64_t)ctas * kRouteThreads * 2) ctas *= 2;
-    return launch_pdl(ctx, route_kernel<ID>, ctas, kRouteThreads, smem, ctas, p);
+    while (ctas < kRouteCluster && p.entries > (int64_t)ctas * threads * 2) ctas *= 2;
+    return p.entries > (int64_t)ctas * threads * kRouteKeep ? route_run<ID, true>(ctx, p, ctas, threads)
+                                                            : route_run<ID, false>(ctx, p, ctas, threads);
 }
 
 sharq_status launch_route(LaunchCtx &ctx, const void *ids, int id_bytes, int64_t tokens, int64_t top_k, int64_t groups,
                           int32_t *offsets, int32_t *rows, int32_t *slots) {
     RouteParams p{ids, tokens * top_k, (int32_t)top_k, (int32_t)groups, offsets, rows, slots};
-    return id_bytes == 8 ? route_run<int64_t>(ctx, p) : route_run<int32_t>(ctx, p);
+    return id_bytes == 8 ? route_any<int64_t>(ctx, p) : route_any<int32_t>(ctx, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -269,10 +321,15 @@ __global__ void __launch_bounds__(kMoveThreads) combine_kernel(const MoveParams 
     }
 }
 
+// Four choices at a time keep a thread within 64 registers, so that four CTAs
+// (32 warps) of an SM overlap their loads, sums and stores: 61 us with eight at
+// a time and two CTAs, 48 us like this (32768 rows of 2048, bf16).
+constexpr int kBackJ = 4;
+
 template <typename T, int VW>
-__global__ void __launch_bounds__(kMoveThreads) combine_bwd_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 4) combine_bwd_kernel(const MoveParams p) {
     using V = Vec<T, VW>;
-    __shared__ float red[kMoveJ][kMoveThreads / 32];
+    __shared__ float red[2][kBackJ][kMoveThreads / 32];
     griddep_wait();
     griddep_launch();
     const int64_t token = blockIdx.x;
@@ -280,47 +337,68 @@ __global__ void __launch_bounds__(kMoveThreads) combine_bwd_kernel(const MovePar
     if (token < p.tokens) {
         const T *y = static_cast<const T *>(p.src), *dout = static_cast<const T *>(p.other) + token * p.k;
         T *dy = static_cast<T *>(p.dst);
-        for (int j0 = 0; j0 < p.top_k; j0 += kMoveJ) {
-            int32_t slot[kMoveJ];
-            float w[kMoveJ], dot[kMoveJ];
+        for (int j0 = 0, parity = 0; j0 < p.top_k; j0 += kBackJ, parity ^= 1) {
+            int32_t slot[kBackJ];
+            float w[kBackJ], dot[kBackJ];
 #pragma unroll
-            for (int j = 0; j < kMoveJ; ++j) {
+            for (int j = 0; j < kBackJ; ++j) {
                 slot[j] = j0 + j < p.top_k ? checked_slot(p, token, j0 + j) : -1;
                 w[j] = slot[j] >= 0 ? p.weights[token * p.top_k + j0 + j] : 0.0f;
                 dot[j] = 0.0f;
             }
             for (int c = threadIdx.x; c < p.k / VW; c += blockDim.x) {
                 const int64_t at = (int64_t)c * VW;
-                typename V::P v[kMoveJ];
-                float d[VW];
+                typename V::P v[kBackJ];
 #pragma unroll
-                for (int j = 0; j < kMoveJ; ++j)
+                for (int j = 0; j < kBackJ; ++j)
                     v[j] = slot[j] >= 0 ? V::load(y + (int64_t)slot[j] * p.k + at) : V::zero();
-                V::unpack(V::load(dout + at), d);
+                const typename V::P dv = V::load(dout + at);
+                if constexpr (VW > 1) {
+                    uint64_t d[VW / 2];
+                    V::unpack2(dv, d);
 #pragma unroll
-                for (int j = 0; j < kMoveJ; ++j) {
-                    if (slot[j] < 0) continue;
-                    float f[VW];
-                    V::unpack(v[j], f);
+                    for (int j = 0; j < kBackJ; ++j) {
+                        if (slot[j] < 0) continue;
+                        uint64_t f[VW / 2], sum = 0;
+                        V::unpack2(v[j], f);
 #pragma unroll
-                    for (int e = 0; e < VW; ++e) dot[j] = fmaf(d[e], f[e], dot[j]);
+                        for (int e = 0; e < VW / 2; ++e) sum = fma2(d[e], f[e], sum);
+                        const float2 t = up2(sum);
+                        dot[j] += t.x + t.y;
+                        const uint64_t w2 = pk2(w[j], w[j]);
 #pragma unroll
-                    for (int e = 0; e < VW; ++e) f[e] = w[j] * d[e];
-                    V::store(dy + (int64_t)slot[j] * p.k + at, V::pack(f));
+                        for (int e = 0; e < VW / 2; ++e) f[e] = mul2(w2, d[e]);
+                        V::store(dy + (int64_t)slot[j] * p.k + at, V::pack2(f));
+                    }
+                } else {
+                    float d[VW];
+                    V::unpack(dv, d);
+#pragma unroll
+                    for (int j = 0; j < kBackJ; ++j) {
+                        if (slot[j] < 0) continue;
+                        float f[VW];
+                        V::unpack(v[j], f);
+                        dot[j] = fmaf(d[0], f[0], dot[j]);
+                        f[0] = w[j] * d[0];
+                        V::store(dy + (int64_t)slot[j] * p.k + at, V::pack(f));
+                    }
                 }
             }
+            // Sums of the four over the warp: lanes 8 q .. 8 q + 7 go on with
+            // the q-th.
+            const bool hi = lane & 16, odd = lane & 8;
+            float a = (hi ? dot[2] : dot[0]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? dot[0] : dot[2], 16);
+            float b = (hi ? dot[3] : dot[1]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? dot[1] : dot[3], 16);
+            float s = (odd ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 8);
 #pragma unroll
-            for (int j = 0; j < kMoveJ; ++j) {
-                const float s = warp_sum(dot[j]);
-                if (lane == 0) red[j][warp] = s;
-            }
+            for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            if ((lane & 7) == 0) red[parity][lane >> 3][warp] = s;
             __syncthreads();
-            if (threadIdx.x < kMoveJ && j0 + (int)threadIdx.x < p.top_k) {
-                float s = 0.0f;
-                for (int i = 0; i < warps; ++i) s += red[threadIdx.x][i];
-                p.dweights[token * p.top_k + j0 + threadIdx.x] = s;
+            if (threadIdx.x < kBackJ && j0 + (int)threadIdx.x < p.top_k) {
+                float t = 0.0f;
+                for (int i = 0; i < warps; ++i) t += red[parity][threadIdx.x][i];
+                p.dweights[token * p.top_k + j0 + threadIdx.x] = t;
             }
-            __syncthreads();
         }
     }
     zero_tail<T, VW>(p);
