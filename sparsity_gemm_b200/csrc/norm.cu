@@ -20,13 +20,17 @@
 namespace sq {
 
 // ---------------------------------------------------------------------------
-// Sums over the threads of a row: one warp, or a CTA through `red` (one slot
-// per warp; each call of a row uses its own array, so one barrier suffices).
+// Sums over the threads of a row: `lanes` (a power of two) neighbouring lanes of
+// a warp, or a CTA through `red` (one slot per warp; each call of a row uses
+// its own array, so one barrier suffices).
 
 template <bool WARP>
-__device__ __forceinline__ float row_sum(float v, float *red) {
+__device__ __forceinline__ float row_sum(float v, float *red, int lanes = 32) {
+    if (WARP) {
+        for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        return v;
+    }
     v = warp_sum(v);
-    if (WARP) return v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     if (lane == 0) red[warp] = v;
     __syncthreads();
@@ -59,6 +63,7 @@ struct NormParams {
     int32_t k;
     float eps;
     int32_t rms;
+    int32_t lanes;  // of a row, where a warp holds whole rows
 };
 
 // Steps on one vector of a row, on packed pairs of binary32 where it holds an
@@ -140,7 +145,8 @@ struct Row {
 
 // A row lives in the registers of its threads (NV vectors of VW elements
 // each, vector i of a thread at i * threads + thread), so x is read once.
-// WARP: one warp per row, kFwdWarps rows per CTA; else one CTA per row.
+// WARP: p.lanes lanes of a warp per row, kFwdWarps warps per CTA; else one CTA
+// per row.
 constexpr int kFwdWarps = 4;
 
 template <typename T, int VW, int NV, bool WARP>
@@ -150,10 +156,15 @@ __global__ void __launch_bounds__(WARP ? 32 * kFwdWarps : 1024) norm_fwd_kernel(
     __shared__ __align__(16) float red[2][32];
     griddep_wait();
     griddep_launch();
-    const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
-    const int threads = WARP ? 32 : blockDim.x;
-    const int64_t row = WARP ? (int64_t)blockIdx.x * kFwdWarps + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
-    if (WARP && row >= p.rows) return;
+    const int threads = WARP ? p.lanes : blockDim.x;
+    const int tid = WARP ? (threadIdx.x & (p.lanes - 1)) : threadIdx.x;
+    int64_t row = blockIdx.x;
+    bool here = true;
+    if (WARP) {
+        row = ((int64_t)blockIdx.x * (32 * kFwdWarps) + threadIdx.x) / p.lanes;
+        here = row < p.rows;
+        if (!here) row = p.rows - 1;  // the warp's shuffles need every lane
+    }
     const int nvec = p.k / VW;
     const T *x = static_cast<const T *>(p.x) + row * p.k;
     T *y = static_cast<T *>(p.y) + row * p.k;
@@ -171,7 +182,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kFwdWarps : 1024) norm_fwd_kernel(
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) s += R::sum(xv[i]);
-        mu = row_sum<WARP>(s, red[0]) * inv_k;
+        mu = row_sum<WARP>(s, red[0], threads) * inv_k;
     }
     float q = 0.0f;
 #pragma unroll
@@ -179,15 +190,15 @@ __global__ void __launch_bounds__(WARP ? 32 * kFwdWarps : 1024) norm_fwd_kernel(
         const float d = R::sum_squares(xv[i], mu);
         if (i * threads + tid < nvec) q += d;
     }
-    const float rstd = rsqrtf(row_sum<WARP>(q, red[1]) * inv_k + p.eps);
-    if (tid == 0) {
+    const float rstd = rsqrtf(row_sum<WARP>(q, red[1], threads) * inv_k + p.eps);
+    if (tid == 0 && here) {
         if (p.mean) p.mean[row] = mu;
         if (p.rstd) p.rstd[row] = rstd;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = i * threads + tid;
-        if (c < nvec) V::store(y + (int64_t)c * VW, R::apply(xv[i], mu, rstd, w, b, c));
+        if (c < nvec && here) V::store(y + (int64_t)c * VW, R::apply(xv[i], mu, rstd, w, b, c));
     }
 }
 
@@ -228,7 +239,8 @@ __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(const NormP
 // ---------------------------------------------------------------------------
 // Backward
 //
-// Persistent row groups (a warp, a CTA, or a cluster of CTAs for long rows)
+// Persistent row groups (some lanes of a warp, a CTA, or a cluster of CTAs for
+// long rows)
 // walk the rows; a thread always owns the same kBwdCols columns, so the
 // weight gradients add up in its registers over all its rows and leave the
 // SM once, as one partial row per CTA; a second kernel adds the partial rows
@@ -237,7 +249,7 @@ constexpr int kBwdCols = 16;          // columns per thread
 constexpr int kBwdThreads = 512;      // most threads of a CTA
 constexpr int kBwdSmall = 256;        // threads up to which an SM holds more than one
 constexpr int kBwdCluster = 8;        // most CTAs of a row
-constexpr int kBwdWarps = 8;          // rows at a time in a CTA of the warp form
+constexpr int kBwdWarps = 8;          // warps of a CTA of the warp form
 
 struct NormBwdParams {
     const void *dy, *x, *w;
@@ -246,6 +258,7 @@ struct NormBwdParams {
     float *part;  // [parts][part_cols]: dw, then db (LayerNorm); NULL: no weight gradients
     int64_t rows, part_cols;
     int32_t k, parts, rms;
+    int32_t lanes;  // of a row in the warp form
 };
 
 template <typename T, int VW, bool WARP>
@@ -254,18 +267,21 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
     constexpr int NV = kBwdCols / VW;
     __shared__ float2 red[2][kBwdThreads / 32];
     __shared__ float2 peer[2][kBwdCluster];
-    extern __shared__ float acc_sm[];  // WARP: [kBwdWarps][2][k]
+    extern __shared__ float acc_sm[];  // WARP: [row groups][2][k]
     griddep_wait();
     griddep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const uint32_t crank = WARP ? 0 : cluster_ctarank();
     uint32_t csize = 1;
     if (!WARP) asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
-    const int tid = WARP ? lane : (int)(crank * blockDim.x + threadIdx.x);
-    const int threads = WARP ? 32 : (int)(csize * blockDim.x);
+    const int threads = WARP ? p.lanes : (int)(csize * blockDim.x);
+    const int tid = WARP ? (lane & (p.lanes - 1)) : (int)(crank * blockDim.x + threadIdx.x);
+    const int groups = WARP ? 32 * kBwdWarps / p.lanes : 1, group = WARP ? (int)threadIdx.x / p.lanes : 0;
     const int part = (int)(blockIdx.x / csize);
-    const int64_t first = WARP ? (int64_t)blockIdx.x * kBwdWarps + warp : (int64_t)part;
-    const int64_t step = WARP ? (int64_t)gridDim.x * kBwdWarps : (int64_t)(gridDim.x / csize);
+    const int64_t first = WARP ? (int64_t)blockIdx.x * groups + group : (int64_t)part;
+    const int64_t step = WARP ? (int64_t)gridDim.x * groups : (int64_t)(gridDim.x / csize);
+    // the warp form's shuffles need every lane: all groups take as many steps
+    const int64_t last = WARP ? (int64_t)blockIdx.x * groups : first;
     const int nvec = p.k / VW;
     const T *xp = static_cast<const T *>(p.x), *dyp = static_cast<const T *>(p.dy), *wp = static_cast<const T *>(p.w);
     T *dxp = static_cast<T *>(p.dx);
@@ -283,6 +299,10 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
     }
     typename V::P xn[NV], dn[NV];
     float mu_n = 0.0f, rs_n = 0.0f;
+    auto clear = [&]() {  // a row that adds nothing
+#pragma unroll
+        for (int i = 0; i < NV; ++i) xn[i] = dn[i] = V::zero();
+    };
     auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -295,8 +315,9 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
         rs_n = __ldg(p.rstd + row);
     };
     if (first < p.rows) fetch(first);
+    else clear();
     int parity = 0;
-    for (int64_t row = first; row < p.rows; row += step, parity ^= 1) {
+    for (int64_t row = first, lead = last; lead < p.rows; row += step, lead += step, parity ^= 1) {
         typename V::P xv[NV], dv[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -305,6 +326,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
         }
         const float mu = mu_n, rs = rs_n;
         if (row + step < p.rows) fetch(row + step);
+        else clear();
         float s1 = 0.0f, s2 = 0.0f;  // sum g, sum g xhat
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -323,9 +345,14 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
                 s2 = fmaf(g, h, s2);
             }
         }
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (!WARP) {
+        if (WARP) {
+            for (int o = p.lanes >> 1; o > 0; o >>= 1) {
+                s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+                s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
+            }
+        } else {
+            s1 = warp_sum(s1);
+            s2 = warp_sum(s2);
             if (lane == 0) red[parity][warp] = make_float2(s1, s2);
             __syncthreads();
             const float2 r = lane < warps ? red[parity][lane] : make_float2(0.0f, 0.0f);
@@ -349,7 +376,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = i * threads + tid;
-            if (c < nvec) {
+            if (c < nvec && row < p.rows) {
                 float xf[VW], df[VW], wf[VW];
                 V::unpack(xv[i], xf);
                 V::unpack(dv[i], df);
@@ -366,7 +393,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
     }
     if (!p.part) return;
     if (WARP) {
-        float *mine = acc_sm + (int64_t)warp * 2 * p.k;
+        float *mine = acc_sm + (int64_t)group * 2 * p.k;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = i * threads + tid;
@@ -380,7 +407,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
         __syncthreads();
         for (int c = threadIdx.x; c < p.part_cols; c += blockDim.x) {
             float s = 0.0f;
-            for (int g = 0; g < kBwdWarps; ++g) s += acc_sm[(int64_t)g * 2 * p.k + c];
+            for (int g = 0; g < groups; ++g) s += acc_sm[(int64_t)g * 2 * p.k + c];
             p.part[(int64_t)blockIdx.x * p.part_cols + c] = s;
         }
     } else {
@@ -585,9 +612,14 @@ static int threads_for(int nvec, int nv) { return (int)round_up((nvec + nv - 1) 
 template <typename T, int VW>
 static sharq_status norm_fwd(LaunchCtx &ctx, const NormParams &p) {
     const int nvec = p.k / VW;
-    const int64_t warp_grid = (p.rows + kFwdWarps - 1) / kFwdWarps;
-    if (nvec <= 32) return launch_pdl(ctx, norm_fwd_kernel<T, VW, 1, true>, warp_grid, 32 * kFwdWarps, 0, 1, p);
-    if (nvec <= 128) return launch_pdl(ctx, norm_fwd_kernel<T, VW, 4, true>, warp_grid, 32 * kFwdWarps, 0, 1, p);
+    if (nvec <= 128) {
+        NormParams q = p;
+        const int nv = nvec <= 64 ? 2 : 4;
+        for (q.lanes = 1; q.lanes * nv < nvec; q.lanes *= 2) {}
+        const int64_t per = 32 * kFwdWarps / q.lanes, grid = (p.rows + per - 1) / per;
+        return nv == 2 ? launch_pdl(ctx, norm_fwd_kernel<T, VW, 2, true>, grid, 32 * kFwdWarps, 0, 1, q)
+                       : launch_pdl(ctx, norm_fwd_kernel<T, VW, 4, true>, grid, 32 * kFwdWarps, 0, 1, q);
+    }
     if (nvec <= 4096) return launch_pdl(ctx, norm_fwd_kernel<T, VW, 4, false>, p.rows, threads_for(nvec, 4), 0, 1, p);
     return launch_pdl(ctx, norm_fwd_long_kernel<T, VW>, p.rows, kLongThreads, 0, 1, p);
 }
@@ -595,7 +627,7 @@ static sharq_status norm_fwd(LaunchCtx &ctx, const NormParams &p) {
 sharq_status launch_layer_norm(LaunchCtx &ctx, const void *x, int64_t rows, int64_t k, const void *w, const void *b,
                                float eps, int norm, int dtype, void *y, float *mean, float *rstd, bool vec16) {
     if (rows == 0) return SHARQ_OK;
-    NormParams p{x, w, b, y, mean, rstd, rows, (int32_t)k, eps, norm};
+    NormParams p{x, w, b, y, mean, rstd, rows, (int32_t)k, eps, norm, 32};
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         return vec16 ? norm_fwd<T, 16 / (int)sizeof(T)>(ctx, p) : norm_fwd<T, 1>(ctx, p);
@@ -608,6 +640,11 @@ static int bwd_cluster(int64_t k) {
     int c = 1;
     while ((int64_t)c * kBwdThreads * kBwdCols < k) c *= 2;
     return c;
+}
+static int bwd_lanes(int64_t k) {  // of a row in the warp form
+    int l = 1;
+    while (l * kBwdCols < k) l *= 2;
+    return l;
 }
 static int bwd_threads(int64_t k, int cluster) {
     return (int)round_up(((k + kBwdCols - 1) / kBwdCols + cluster - 1) / cluster, 32);
@@ -625,20 +662,22 @@ int64_t norm_bwd_parts(int64_t rows, int64_t k) {
     if (rows <= 0) return 0;
     const int64_t sms = 148;
     if (k <= 32 * kBwdCols) {
-        const int64_t need = (rows + kBwdWarps - 1) / kBwdWarps;
+        const int64_t per = 32 * kBwdWarps / bwd_lanes(k), need = (rows + per - 1) / per;
         return need < 2 * sms ? need : 2 * sms;
     }
     const int cluster = bwd_cluster(k);
     const int64_t most = bwd_per_sm(bwd_threads(k, cluster)) * sms / cluster;
-    const int64_t few = rows <= 64 ? rows : rows / 6 < 64 ? 64 : rows / 6;
+    const int64_t few = rows <= 64 ? rows : rows / 4 < 64 ? 64 : rows / 4;
     return few < most ? few : most;
 }
 
 template <typename T, int VW>
 static sharq_status norm_bwd(LaunchCtx &ctx, const NormBwdParams &p) {
     if (p.k <= 32 * kBwdCols) {
-        const size_t smem = (size_t)kBwdWarps * 2 * p.k * sizeof(float);  // at most 32 KB
-        return launch_pdl(ctx, norm_bwd_kernel<T, VW, true>, p.parts, 32 * kBwdWarps, smem, 1, p);
+        NormBwdParams q = p;
+        q.lanes = bwd_lanes(p.k);
+        const size_t smem = (size_t)(32 * kBwdWarps / q.lanes) * 2 * p.k * sizeof(float);  // at most 32 KB
+        return launch_pdl(ctx, norm_bwd_kernel<T, VW, true>, p.parts, 32 * kBwdWarps, smem, 1, q);
     }
     const int cluster = bwd_cluster(p.k), threads = bwd_threads(p.k, cluster);
     if constexpr (VW > 1) {
@@ -669,7 +708,7 @@ sharq_status launch_layer_norm_backward(LaunchCtx &ctx, const void *dy, const vo
     const bool grads = dw || db;
     const int64_t cols = norm == 1 ? k : 2 * k;  // RMSNorm has no db
     if (rows > 0) {
-        NormBwdParams p{dy, x, w, mean, rstd, dx, grads ? part : nullptr, rows, cols, (int32_t)k, parts, norm};
+        NormBwdParams p{dy, x, w, mean, rstd, dx, grads ? part : nullptr, rows, cols, (int32_t)k, parts, norm, 32};
         const sharq_status st = with_dtype(dtype, [&](auto t) {
             using T = decltype(t);
             return vec16 ? norm_bwd<T, 16 / (int)sizeof(T)>(ctx, p) : norm_bwd<T, 1>(ctx, p);
