@@ -568,29 +568,41 @@ def _refuse(t, name: str, dev: int, dtype, shape, rows: bool):
     _require(t.get_device() == dev, f"{name} must be on the device of the first argument")
 
 
+def _current() -> int:
+    return torch.cuda.current_device()
+
+
 def _first(t, name: str, dims: int = 2, rows: bool = False, dtype=None) -> int:
     """Checks the tensor that fixes a call's type and device; the device."""
-    if not (isinstance(t, torch.Tensor) and t.dim() == dims and (t.dtype in _DTYPES if dtype is None else t.dtype == dtype)
-            and (rows or t.is_contiguous()) and t.is_cuda and t.get_device() == torch.cuda.current_device()):
-        _refuse(t, name, t.get_device() if isinstance(t, torch.Tensor) else -1, dtype, (None,) * dims, rows)
-    return t.get_device()
+    try:
+        dev = t.get_device()
+        if (dev >= 0 and t.dim() == dims and (t.dtype is dtype or (dtype is None and t.dtype in _DTYPES))
+                and (rows or t.is_contiguous()) and dev == _current()):
+            return dev
+    except AttributeError:
+        dev = -1
+    _refuse(t, name, dev, dtype, (None,) * dims, rows)
+    return dev
 
 
 def _take(t, name: str, dev: int, dtype, shape, rows: bool = False):
     """Checks a tensor: device, type, shape, and contiguous (rows: rows of
     consecutive elements that do not overlap)."""
-    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype == dtype and t.shape == shape
-            and t.is_contiguous()):
-        _refuse(t, name, dev, dtype, shape, rows)
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _refuse(t, name, dev, dtype, shape, rows)
 
 
-def _no_grad_inputs(*ts):
+def _no_grad(*ts):
     """The calls below are not recorded by autograd; a call that would lose a
     gradient silently is refused (the *_backward calls are the gradients)."""
-    if torch.is_grad_enabled():
-        for t in ts:
-            _require(t is None or not t.requires_grad,
-                     "inputs that require a gradient are refused: call under torch.no_grad() and use the backward calls")
+    for t in ts:
+        if t is not None and t.requires_grad:
+            raise ValueError("inputs that require a gradient are refused: call under torch.no_grad() and use the "
+                             "backward calls")
 
 
 def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
@@ -621,8 +633,10 @@ def _at(t):
 
 
 def _norm_kind(norm: str) -> int:
-    _require(norm == "layer" or norm == "rms", 'norm must be "layer" or "rms"')
-    return 1 if norm == "rms" else 0
+    if norm == "layer":
+        return 0
+    _require(norm == "rms", 'norm must be "layer" or "rms"')
+    return 1
 
 
 def layer_norm(x: torch.Tensor, w=None, b=None, eps: float = 1e-5, norm: str = "layer", stats: bool = False,
@@ -640,7 +654,8 @@ def layer_norm(x: torch.Tensor, w=None, b=None, eps: float = 1e-5, norm: str = "
     if b is not None:
         _require(kind == 0, "RMSNorm takes no b")
         _take(b, "b", dev, dt, (k,))
-    _no_grad_inputs(x, w, b)
+    if torch.is_grad_enabled():
+        _no_grad(x, w, b)
     if out is None:
         out = _new_like(x, stream)
     else:
@@ -649,7 +664,7 @@ def layer_norm(x: torch.Tensor, w=None, b=None, eps: float = 1e-5, norm: str = "
     if stats:
         mean = _new(x, (m_tok,), _f32, stream) if kind == 0 else None
         rstd = _new(x, (m_tok,), _f32, stream)
-    st = lib().sharq_layer_norm(x.data_ptr(), m_tok, k, _at(w), _at(b), eps, kind, _DTYPES[dt], out.data_ptr(), _at(mean),
+    st = (_lib or lib()).sharq_layer_norm(x.data_ptr(), m_tok, k, _at(w), _at(b), eps, kind, _DTYPES[dt], out.data_ptr(), _at(mean),
                                 _at(rstd), _raw(stream, dev))
     if st:
         _check(st, "sharq_layer_norm")
@@ -678,7 +693,8 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean, rstd: torch.Ten
     _take(rstd, "rstd", dev, _f32, (m_tok,))
     if w is not None:
         _take(w, "w", dev, dt, (k,))
-    _no_grad_inputs(dy, x, w)
+    if torch.is_grad_enabled():
+        _no_grad(dy, x, w)
     if out is None:
         out = _new_like(x, stream)
     else:
@@ -692,7 +708,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean, rstd: torch.Ten
         dw = _new(x, (k,), _f32, stream)
         db = _new(x, (k,), _f32, stream) if kind == 0 else None
         ws = _new(x, (nbytes,), torch.uint8, stream)
-    st = lib().sharq_layer_norm_backward(dy.data_ptr(), x.data_ptr(), m_tok, k, _at(w), _at(mean), rstd.data_ptr(), kind,
+    st = (_lib or lib()).sharq_layer_norm_backward(dy.data_ptr(), x.data_ptr(), m_tok, k, _at(w), _at(mean), rstd.data_ptr(), kind,
                                          _DTYPES[dt], out.data_ptr(), _at(dw), _at(db), _at(ws), nbytes, _raw(stream, dev))
     if st:
         _check(st, "sharq_layer_norm_backward")
@@ -719,8 +735,9 @@ class Routing:
 
 
 def _routing(r, dev: int):
-    _require(isinstance(r, Routing), "routing must be a Routing (from route)")
-    _require(r.dev == dev, f"routing is on cuda:{r.dev}, the tensors on cuda:{dev}")
+    if not isinstance(r, Routing) or r.dev != dev:
+        _require(isinstance(r, Routing), "routing must be a Routing (from route)")
+        _require(False, f"routing is on cuda:{r.dev}, the tensors on cuda:{dev}")
 
 
 def route(ids: torch.Tensor, groups: int, stream=None) -> Routing:
@@ -737,7 +754,7 @@ def route(ids: torch.Tensor, groups: int, stream=None) -> Routing:
     r.offsets = _new(ids, (groups + 1,), _i32, stream)
     r.rows = _new(ids, (m_tok * top_k,), _i32, stream)
     r.slots = _new(ids, (m_tok, top_k), _i32, stream)
-    st = lib().sharq_route(ids.data_ptr(), ids.element_size(), m_tok, top_k, groups, r.offsets.data_ptr(),
+    st = (_lib or lib()).sharq_route(ids.data_ptr(), ids.element_size(), m_tok, top_k, groups, r.offsets.data_ptr(),
                            r.rows.data_ptr(), r.slots.data_ptr(), _raw(stream, dev))
     if st:
         _check(st, "sharq_route")
@@ -752,13 +769,14 @@ def permute_rows(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = N
     _routing(routing, dev)
     m_tok, k = x.shape
     _require(routing.m_tok == m_tok, "routing is of another number of tokens")
-    _no_grad_inputs(x)
+    if x.requires_grad and torch.is_grad_enabled():
+        _no_grad(x)
     shape = (m_tok * routing.top_k, k)
     if out is None:
         out = _new(x, shape, x.dtype, stream)
     else:
         _take(out, "out", dev, x.dtype, shape)
-    st = lib().sharq_permute_rows(x.data_ptr(), m_tok, k, routing.slots.data_ptr(), routing.top_k,
+    st = (_lib or lib()).sharq_permute_rows(x.data_ptr(), m_tok, k, routing.slots.data_ptr(), routing.top_k,
                                   routing.offsets.data_ptr(), routing.groups, _DTYPES[x.dtype], out.data_ptr(),
                                   _raw(stream, dev))
     if st:
@@ -779,12 +797,13 @@ def combine(y: torch.Tensor, routing: Routing, weights: torch.Tensor | None = No
         _take(weights, "weights", dev, _f32, (m_tok, top_k))
     if residual is not None:
         _take(residual, "residual", dev, dt, (m_tok, k))
-    _no_grad_inputs(y, weights, residual)
+    if torch.is_grad_enabled():
+        _no_grad(y, weights, residual)
     if out is None:
         out = _new(y, (m_tok, k), dt, stream)
     else:
         _take(out, "out", dev, dt, (m_tok, k))
-    st = lib().sharq_combine(y.data_ptr(), rows, m_tok, k, routing.slots.data_ptr(), _at(weights), top_k, _at(residual),
+    st = (_lib or lib()).sharq_combine(y.data_ptr(), rows, m_tok, k, routing.slots.data_ptr(), _at(weights), top_k, _at(residual),
                              _DTYPES[dt], out.data_ptr(), _raw(stream, dev))
     if st:
         _check(st, "sharq_combine")
@@ -802,10 +821,11 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, routing: Routing, weig
     rows, k = y.shape
     _take(dout, "dout", dev, dt, (m_tok, k))
     _take(weights, "weights", dev, _f32, (m_tok, top_k))
-    _no_grad_inputs(dout, y, weights)
+    if torch.is_grad_enabled():
+        _no_grad(dout, y, weights)
     dy = _new_like(y, stream)
     dweights = _new_like(weights, stream)
-    st = lib().sharq_combine_backward(dout.data_ptr(), y.data_ptr(), rows, m_tok, k, routing.slots.data_ptr(),
+    st = (_lib or lib()).sharq_combine_backward(dout.data_ptr(), y.data_ptr(), rows, m_tok, k, routing.slots.data_ptr(),
                                       weights.data_ptr(), top_k, routing.offsets.data_ptr(), routing.groups, _DTYPES[dt],
                                       dy.data_ptr(), dweights.data_ptr(), _raw(stream, dev))
     if st:
@@ -849,7 +869,8 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, routing: Routing, sc
     if base is not None:
         _take(base, "base", dev, dt, (m_tok, n_out), True)
         ldbase = base.stride(0) if m_tok > 1 else n_out
-    _no_grad_inputs(x, a, b, scales, base)
+    if torch.is_grad_enabled():
+        _no_grad(x, a, b, scales, base)
     if out is None:
         out = _new(x, (m_tok, n_out), dt, stream)
         ldo = n_out
@@ -862,7 +883,7 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, routing: Routing, sc
              "x, a, b, base and out must be 16-byte aligned, with row strides that are multiples of 8")
     nbytes = _lora_bytes(m_tok, rank, groups)
     ws = _new(x, (nbytes,), torch.uint8, stream) if nbytes else None
-    st = lib().sharq_lora(px, ldx, m_tok, k, pa, pb, n_out, rank, groups, _at(scales), routing.offsets.data_ptr(),
+    st = (_lib or lib()).sharq_lora(px, ldx, m_tok, k, pa, pb, n_out, rank, groups, _at(scales), routing.offsets.data_ptr(),
                           routing.rows.data_ptr(), routing.slots.data_ptr(), _DTYPES[dt], pbase, ldbase, pout, ldo,
                           _at(ws), nbytes, _raw(stream, dev))
     if st:

@@ -515,7 +515,7 @@ constexpr int kShX = kShRows * kShK * 2;
 template <int R>
 struct ShrinkCfg {
     static constexpr int kStage = kShX + R * kShK * 2;
-    static constexpr int kStages = 100 * 1024 / kStage;  // two CTAs on an SM
+    static constexpr int kStages = (R <= 64 ? 72 : 100) * 1024 / kStage;  // two CTAs on an SM
     static constexpr int kLd = R + 4;                    // row stride of the binary32 parts
     static constexpr int kPart = kShRows * kLd * 4;
     static constexpr int kSmem = 1024 + (kStages * kStage > kPart ? kStages * kStage : kPart);

@@ -131,6 +131,7 @@ def here(monkeypatch):
     for name in ("layer_norm", "layer_norm_backward", "route", "permute_rows", "combine", "combine_backward", "lora"):
         getattr(fake, "sharq_" + name).return_value = sq.OK
     monkeypatch.setattr(sq, "lib", lambda: fake)
+    monkeypatch.setattr(sq, "_lib", None)
     monkeypatch.setattr(sq, "_new", lambda like, shape, dtype, stream: _as_cuda(torch.zeros(shape, dtype=dtype)))
     monkeypatch.setattr(sq, "_new_like", lambda t, stream: _as_cuda(torch.zeros(t.shape, dtype=t.dtype)))
     monkeypatch.setattr(sq, "_raw", lambda stream, dev: 0)
