@@ -553,7 +553,8 @@ sharq_status sharq_layer_norm(const void *x_dev, int64_t m_tok, int64_t k, const
  *   dx_dev              [m_tok][k] of the element type; may be dy_dev itself.
  *   dw_dev, db_dev      float [k], or NULL; written (zero) for m_tok == 0 too.
  *   ws_dev              workspace of sharq_layer_norm_backward_bytes(m_tok, k)
- *                       bytes, 256-byte aligned; NULL if dw and db are NULL.
+ *                       bytes, 256-byte aligned; may be NULL where dw and db
+ *                       are NULL and k <= 8192 (longer rows take two passes).
  */
 size_t sharq_layer_norm_backward_bytes(int64_t m_tok, int64_t k);
 sharq_status sharq_layer_norm_backward(const void *dy_dev, const void *x_dev, int64_t m_tok, int64_t k,

@@ -701,13 +701,14 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean, rstd: torch.Ten
         _take(out, "out", dev, dt, (m_tok, k))
     dw = db = ws = None
     nbytes = 0
-    if w is not None:
+    if w is not None or k > 8192:  # longer rows take two passes
         nbytes = _norm_backward_bytes(m_tok, k)
         if nbytes == 0:
             raise SharqError(ERR_INVALID_ARG, f"layer_norm_backward shape {tuple(x.shape)}")
+        ws = _new(x, (nbytes,), torch.uint8, stream)
+    if w is not None:
         dw = _new(x, (k,), _f32, stream)
         db = _new(x, (k,), _f32, stream) if kind == 0 else None
-        ws = _new(x, (nbytes,), torch.uint8, stream)
     st = (_lib or lib()).sharq_layer_norm_backward(dy.data_ptr(), x.data_ptr(), m_tok, k, _at(w), _at(mean), rstd.data_ptr(), kind,
                                          _DTYPES[dt], out.data_ptr(), _at(dw), _at(db), _at(ws), nbytes, _raw(stream, dev))
     if st:

@@ -616,7 +616,7 @@ sharq_status sharq_layer_norm(const void *x_dev, int64_t m_tok, int64_t k, const
 
 size_t sharq_layer_norm_backward_bytes(int64_t m_tok, int64_t k) {
     if (!rows_ok(m_tok) || !width_ok(k)) return 0;
-    const int64_t b = sq::norm_bwd_parts(m_tok, k) * 2 * k * (int64_t)sizeof(float);
+    const int64_t b = sq::norm_bwd_bytes(m_tok, k);
     return (size_t)sq::round_up(b > 0 ? b : 1, sq::kAlign);
 }
 
@@ -638,8 +638,8 @@ sharq_status sharq_layer_norm_backward(const void *dy_dev, const void *x_dev, in
             return SHARQ_ERR_INVALID_ARG;
     }
     if ((dw_dev && !aligned(dw_dev, 4)) || (db_dev && !aligned(db_dev, 4))) return SHARQ_ERR_INVALID_ARG;
-    if (dw_dev || db_dev) {
-        if (overlap(dw_dev, 4 * k, db_dev, 4 * k)) return SHARQ_ERR_INVALID_ARG;
+    if (overlap(dw_dev, 4 * k, db_dev, 4 * k)) return SHARQ_ERR_INVALID_ARG;
+    if (dw_dev || db_dev || !sq::norm_bwd_one_pass(k)) {
         if (m_tok > 0 && (!ws_dev || !aligned(ws_dev, sq::kAlign) || ws_bytes < sharq_layer_norm_backward_bytes(m_tok, k)))
             return SHARQ_ERR_INVALID_ARG;
     }
@@ -649,7 +649,7 @@ sharq_status sharq_layer_norm_backward(const void *dy_dev, const void *x_dev, in
     sharq_status st = make_ctx(stream, ctx);
     if (st != SHARQ_OK) return st;
     st = sq::launch_layer_norm_backward(ctx, dy_dev, x_dev, m_tok, k, ln_w_dev, mean_dev, rstd_dev, norm, dtype, dx_dev,
-                                        dw_dev, db_dev, static_cast<float *>(ws_dev), vec16);
+                                        dw_dev, db_dev, ws_dev, vec16);
     g_last_launches = ctx.launches;
     return st;
 }

@@ -239,16 +239,16 @@ __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(const NormP
 // ---------------------------------------------------------------------------
 // Backward
 //
-// Persistent row groups (some lanes of a warp, a CTA, or a cluster of CTAs for
-// long rows)
-// walk the rows; a thread always owns the same kBwdCols columns, so the
-// weight gradients add up in its registers over all its rows and leave the
-// SM once, as one partial row per CTA; a second kernel adds the partial rows
-// in their order. The next row is loaded before the current one is reduced.
+// Persistent row groups (some lanes of a warp, or a CTA) walk the rows; a
+// thread always owns the same kBwdCols columns, so the weight gradients add up
+// in its registers over all its rows and leave the SM once, as one partial row
+// per CTA; a second kernel adds the partial rows in their order. The next row
+// is loaded before the current one is reduced. Rows longer than a CTA's
+// registers take two passes, at the end of this section.
 constexpr int kBwdCols = 16;          // columns per thread
 constexpr int kBwdThreads = 512;      // most threads of a CTA
 constexpr int kBwdSmall = 256;        // threads up to which an SM holds more than one
-constexpr int kBwdCluster = 8;        // most CTAs of a row
+constexpr int kBwdRow = kBwdThreads * kBwdCols;  // longest row of one pass
 constexpr int kBwdWarps = 8;          // warps of a CTA of the warp form
 
 struct NormBwdParams {
@@ -259,6 +259,7 @@ struct NormBwdParams {
     int64_t rows, part_cols;
     int32_t k, parts, rms;
     int32_t lanes;  // of a row in the warp form
+    float2 *sums;   // rows in two passes: each row's means of g and of g xhat
 };
 
 template <typename T, int VW, bool WARP>
@@ -266,27 +267,22 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
     using V = Vec<T, VW>;
     constexpr int NV = kBwdCols / VW;
     __shared__ float2 red[2][kBwdThreads / 32];
-    __shared__ float2 peer[2][kBwdCluster];
     extern __shared__ float acc_sm[];  // WARP: [row groups][2][k]
     griddep_wait();
     griddep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const uint32_t crank = WARP ? 0 : cluster_ctarank();
-    uint32_t csize = 1;
-    if (!WARP) asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
-    const int threads = WARP ? p.lanes : (int)(csize * blockDim.x);
-    const int tid = WARP ? (lane & (p.lanes - 1)) : (int)(crank * blockDim.x + threadIdx.x);
+    const int threads = WARP ? p.lanes : (int)blockDim.x;
+    const int tid = WARP ? (lane & (p.lanes - 1)) : (int)threadIdx.x;
     const int groups = WARP ? 32 * kBwdWarps / p.lanes : 1, group = WARP ? (int)threadIdx.x / p.lanes : 0;
-    const int part = (int)(blockIdx.x / csize);
+    const int part = (int)blockIdx.x;
     const int64_t first = WARP ? (int64_t)blockIdx.x * groups + group : (int64_t)part;
-    const int64_t step = WARP ? (int64_t)gridDim.x * groups : (int64_t)(gridDim.x / csize);
+    const int64_t step = WARP ? (int64_t)gridDim.x * groups : (int64_t)gridDim.x;
     // the warp form's shuffles need every lane: all groups take as many steps
     const int64_t last = WARP ? (int64_t)blockIdx.x * groups : first;
     const int nvec = p.k / VW;
     const T *xp = static_cast<const T *>(p.x), *dyp = static_cast<const T *>(p.dy), *wp = static_cast<const T *>(p.w);
     T *dxp = static_cast<T *>(p.dx);
     const float inv_k = 1.0f / (float)p.k;
-    if (csize > 1) cluster_sync();  // every CTA of the row runs before another writes to its shared memory
 
     typename V::P wv[NV];
     float dw[kBwdCols], db[kBwdCols];
@@ -358,19 +354,6 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
             const float2 r = lane < warps ? red[parity][lane] : make_float2(0.0f, 0.0f);
             s1 = warp_sum(r.x);
             s2 = warp_sum(r.y);
-            if (csize > 1) {  // every CTA of the row gets every CTA's sums, added in rank order
-                if (threadIdx.x < csize) {
-                    const uint32_t at = mapa_shared(smem_u32(&peer[parity][crank]), threadIdx.x);
-                    st_cluster_u32(at, __float_as_uint(s1));
-                    st_cluster_u32(at + 4, __float_as_uint(s2));
-                }
-                cluster_sync();
-                s1 = s2 = 0.0f;
-                for (uint32_t c = 0; c < csize; ++c) {
-                    s1 += peer[parity][c].x;
-                    s2 += peer[parity][c].y;
-                }
-            }
         }
         const float m1 = p.rms ? 0.0f : s1 * inv_k, m2 = s2 * inv_k;
 #pragma unroll
@@ -425,10 +408,13 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
     }
 }
 
-// The form for rows of whole 16-byte vectors: a CTA (or a cluster, each CTA
-// with its part of the columns) per row, kBwdCols columns per thread, and a
-// ring of rows of x and dy filled by bulk copies several rows ahead. The
-// barrier of a row's reduction also frees its ring slot.
+// The form for rows of whole 16-byte vectors: a CTA per row, kBwdCols columns
+// per thread, and a ring of rows of x and dy filled by bulk copies several rows
+// ahead. The barrier of a row's reduction also frees its ring slot. Bound by
+// instructions and their latency (half the issue slots at 16 warps per SM;
+// fewer columns per thread and more warps measured slower: 8192 x 4096 in bf16
+// takes 37 us like this, 56 with 8 columns): 73% of the copy rate with the
+// reduction of the partial rows.
 constexpr int kRingMax = 8;            // most rows in a ring
 constexpr int kRingBytes = 160 << 10;  // shared memory of an SM's rings
 
@@ -441,29 +427,22 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kBwdSmall ? 2 : 1)
     extern __shared__ __align__(128) uint8_t ring[];  // [stages][x, dy][part of a row]
     __shared__ uint64_t full[kRingMax];
     __shared__ __align__(16) float2 red[2][MAXT / 32];
-    __shared__ float2 peer[2][kBwdCluster];
     griddep_wait();
     griddep_launch();
     const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t crank = cluster_ctarank();
-    uint32_t csize;
-    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
-    const int per = (p.k / VW + (int)csize - 1) / (int)csize;  // vectors of a CTA
-    const int v0 = (int)crank * per, cnt = max(0, min(per, p.k / VW - v0));
-    const uint32_t bytes = (uint32_t)cnt * 16, stride = (uint32_t)per * 16;
-    const int64_t part = blockIdx.x / csize, parts = gridDim.x / csize;
+    const int cnt = p.k / VW;  // vectors of a row
+    const uint32_t bytes = (uint32_t)cnt * 16;
+    const int64_t part = blockIdx.x, parts = gridDim.x;
     const int iters = (int)((p.rows - part + parts - 1) / parts);
-    const T *xp = static_cast<const T *>(p.x) + (int64_t)v0 * VW, *dyp = static_cast<const T *>(p.dy) + (int64_t)v0 * VW;
+    const T *xp = static_cast<const T *>(p.x), *dyp = static_cast<const T *>(p.dy);
     const T *wp = static_cast<const T *>(p.w);
-    T *dxp = static_cast<T *>(p.dx) + (int64_t)v0 * VW;
+    T *dxp = static_cast<T *>(p.dx);
     auto issue = [&](int it, int s) {
         const int64_t at = (part + it * parts) * p.k;
-        const uint32_t dst = smem_u32(ring) + s * 2 * stride, bar = smem_u32(&full[s]);
+        const uint32_t dst = smem_u32(ring) + s * 2 * bytes, bar = smem_u32(&full[s]);
         mbar_arrive_expect_tx(bar, 2 * bytes);
-        if (bytes) {
-            bulk_load(dst, xp + at, bytes, bar);
-            bulk_load(dst + stride, dyp + at, bytes, bar);
-        }
+        bulk_load(dst, xp + at, bytes, bar);
+        bulk_load(dst + bytes, dyp + at, bytes, bar);
     };
     if (tid == 0) {
         for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&full[s]), 1);
@@ -471,7 +450,6 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kBwdSmall ? 2 : 1)
     }
     if (tid < 2 * (MAXT / 32)) red[tid / (MAXT / 32)][tid % (MAXT / 32)] = make_float2(0.0f, 0.0f);  // warps not there
     __syncthreads();
-    if (csize > 1) cluster_sync();  // every CTA of the row runs before another writes to its shared memory
     if (tid == 0)
         for (int it = 0; it < stages && it < iters; ++it) issue(it, it);
     const float inv_k = 1.0f / (float)p.k;
@@ -479,7 +457,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kBwdSmall ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = i * threads + tid;
-        V::unpack2(wp && (FULL || c < cnt) ? V::load(wp + (int64_t)(v0 + c) * VW) : V::ones(), wf[i]);
+        V::unpack2(wp && (FULL || c < cnt) ? V::load(wp + (int64_t)c * VW) : V::ones(), wf[i]);
 #pragma unroll
         for (int e = 0; e < H; ++e) dw[i][e] = db[i][e] = 0;
     }
@@ -501,11 +479,11 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kBwdSmall ? 2 : 1)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = i * threads + tid;
-            const uint8_t *at = ring + slot * 2 * stride + c * 16;
+            const uint8_t *at = ring + slot * 2 * bytes + c * 16;
             uint64_t df[H];
             // columns past the row: dy = 0, so they add nothing
             V::unpack2(FULL || c < cnt ? *reinterpret_cast<const typename V::P *>(at) : V::zero(), h[i]);
-            V::unpack2(FULL || c < cnt ? *reinterpret_cast<const typename V::P *>(at + stride) : V::zero(), df);
+            V::unpack2(FULL || c < cnt ? *reinterpret_cast<const typename V::P *>(at + bytes) : V::zero(), df);
 #pragma unroll
             for (int e = 0; e < H; ++e) {
                 h[i][e] = mul2(add2(h[i][e], mu2), rs2);
@@ -535,19 +513,6 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kBwdSmall ? 2 : 1)
             s1 += r.x + r.z;
             s2 += r.y + r.w;
         }
-        if (csize > 1) {  // every CTA of the row gets every CTA's sums, added in rank order
-            if ((uint32_t)tid < csize) {
-                const uint32_t at = mapa_shared(smem_u32(&peer[parity][crank]), (uint32_t)tid);
-                st_cluster_u32(at, __float_as_uint(s1));
-                st_cluster_u32(at + 4, __float_as_uint(s2));
-            }
-            cluster_sync();
-            s1 = s2 = 0.0f;
-            for (uint32_t c = 0; c < csize; ++c) {
-                s1 += peer[parity][c].x;
-                s2 += peer[parity][c].y;
-            }
-        }
         const float m1 = p.rms ? 0.0f : s1 * inv_k, m2 = s2 * inv_k;
         const uint64_t m1n = pk2(-m1 * rs, -m1 * rs), m2n = pk2(-m2, -m2);
 #pragma unroll
@@ -571,36 +536,185 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kBwdSmall ? 2 : 1)
         if (c < cnt)
 #pragma unroll
             for (int e = 0; e < H; ++e) {
-                *reinterpret_cast<float2 *>(mine + (v0 + c) * VW + 2 * e) = up2(dw[i][e]);
-                if (!p.rms) *reinterpret_cast<float2 *>(mine + p.k + (v0 + c) * VW + 2 * e) = up2(db[i][e]);
+                *reinterpret_cast<float2 *>(mine + c * VW + 2 * e) = up2(dw[i][e]);
+                if (!p.rms) *reinterpret_cast<float2 *>(mine + p.k + c * VW + 2 * e) = up2(db[i][e]);
             }
     }
 }
 
-// dw and db: column sums of the partial rows. A CTA takes 32 columns; its 32
-// warps add every 32nd partial row, then the 32 sums are added in order.
-__global__ void __launch_bounds__(1024) norm_bwd_reduce_kernel(const float *part, int parts, int64_t cols, int k, float *dw,
-                                                               float *db) {
-    __shared__ float sum[32][33];
+// Rows longer than kBwdRow: their sums first (a CTA per row), then dx and the
+// weight gradients by columns (a CTA takes kColThreads x kColVecs vectors of
+// some rows, and no thread waits for another). x and dy are read twice, the
+// second time from L2 where they fit. (Clusters with a part of the columns per
+// CTA read them once, but a cluster barrier per row costs more: 1024 x 14336 in
+// bf16 took 43 us, 512 x 20000 62 us, against 35 and 26 like this.)
+constexpr int kColThreads = 256;
+constexpr int kColRows = 4;  // rows in flight
+
+template <typename T, int VW>
+__global__ void __launch_bounds__(kBwdThreads) norm_bwd_sums_kernel(const NormBwdParams p) {
+    using V = Vec<T, VW>;
+    __shared__ __align__(16) float red[2][32];
+    griddep_wait();
+    griddep_launch();
+    const int64_t row = blockIdx.x;
+    const T *x = static_cast<const T *>(p.x) + row * p.k, *dy = static_cast<const T *>(p.dy) + row * p.k;
+    const T *w = static_cast<const T *>(p.w);
+    const float mu = p.rms ? 0.0f : p.mean[row], rs = p.rstd[row];
+    float s1 = 0.0f, s2 = 0.0f;
+    const uint64_t mu2 = pk2(-mu, -mu), rs2 = pk2(rs, rs);
+#pragma unroll 4
+    for (int c = threadIdx.x; c < p.k / VW; c += kBwdThreads) {
+        const typename V::P xv = V::load(x + (int64_t)c * VW), dv = V::load(dy + (int64_t)c * VW);
+        const typename V::P wv = w ? V::load(w + (int64_t)c * VW) : V::ones();
+        if constexpr (VW > 1) {
+            uint64_t xf[VW / 2], df[VW / 2], wf[VW / 2], t1 = 0, t2 = 0;
+            V::unpack2(xv, xf);
+            V::unpack2(dv, df);
+            V::unpack2(wv, wf);
+#pragma unroll
+            for (int e = 0; e < VW / 2; ++e) {
+                const uint64_t g = mul2(df[e], wf[e]);
+                t1 = add2(t1, g);
+                t2 = fma2(g, mul2(add2(xf[e], mu2), rs2), t2);
+            }
+            const float2 a = up2(t1), b = up2(t2);
+            s1 += a.x + a.y;
+            s2 += b.x + b.y;
+        } else {
+            float xf[VW], df[VW], wf[VW];
+            V::unpack(xv, xf);
+            V::unpack(dv, df);
+            V::unpack(wv, wf);
+            const float g = df[0] * wf[0];
+            s1 += g;
+            s2 = fmaf(g, (xf[0] - mu) * rs, s2);
+        }
+    }
+    s1 = row_sum<false>(s1, red[0]);
+    s2 = row_sum<false>(s2, red[1]);
+    const float inv_k = 1.0f / (float)p.k;
+    if (threadIdx.x == 0) p.sums[row] = make_float2(p.rms ? 0.0f : s1 * inv_k, s2 * inv_k);
+}
+
+template <typename T, int VW, int NV>
+__global__ void __launch_bounds__(kColThreads) norm_bwd_cols_kernel(const NormBwdParams p) {
+    using V = Vec<T, VW>;
+    griddep_wait();
+    griddep_launch();
+    const int nvec = p.k / VW, across = (nvec + kColThreads * NV - 1) / (kColThreads * NV);
+    const int64_t part = blockIdx.x / across;
+    const int v0 = (int)(blockIdx.x % across) * kColThreads * NV + (int)threadIdx.x;
+    const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy), *w = static_cast<const T *>(p.w);
+    T *dx = static_cast<T *>(p.dx);
+    constexpr int H = (VW + 1) / 2;  // packed pairs (a single value: the pair's first)
+    uint64_t wf[NV][H], dw[NV][H], db[NV][H];
+    auto widen2 = [](typename V::P v, uint64_t (&f)[H]) {
+        if constexpr (VW > 1) {
+            V::unpack2(v, f);
+        } else {
+            float t[VW];
+            V::unpack(v, t);
+            f[0] = pk2(t[0], 0.0f);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = v0 + i * kColThreads;
+        widen2(w && c < nvec ? V::load(w + (int64_t)c * VW) : V::ones(), wf[i]);
+#pragma unroll
+        for (int e = 0; e < H; ++e) dw[i][e] = db[i][e] = 0;
+    }
+    for (int64_t r0 = part; r0 < p.rows; r0 += (int64_t)kColRows * p.parts) {
+        typename V::P xv[kColRows][NV], dv[kColRows][NV];
+        float mu[kColRows], rs[kColRows];
+        float2 m[kColRows];
+#pragma unroll
+        for (int j = 0; j < kColRows; ++j) {
+            const int64_t row = r0 + (int64_t)j * p.parts;
+            const bool in = row < p.rows;
+            mu[j] = in && !p.rms ? p.mean[row] : 0.0f;
+            rs[j] = in ? p.rstd[row] : 0.0f;
+            m[j] = in ? p.sums[row] : make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = v0 + i * kColThreads;
+                const bool here = in && c < nvec;
+                xv[j][i] = here ? V::load(x + row * p.k + (int64_t)c * VW) : V::zero();
+                dv[j][i] = here ? V::load(dy + row * p.k + (int64_t)c * VW) : V::zero();
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kColRows; ++j) {
+            const int64_t row = r0 + (int64_t)j * p.parts;
+            const uint64_t mu2 = pk2(-mu[j], -mu[j]), rs2 = pk2(rs[j], rs[j]), m2n = pk2(-m[j].y, -m[j].y);
+            const uint64_t m1n = pk2(-m[j].x * rs[j], -m[j].x * rs[j]);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = v0 + i * kColThreads;
+                uint64_t h[H], df[H];
+                widen2(xv[j][i], h);
+                widen2(dv[j][i], df);
+#pragma unroll
+                for (int e = 0; e < H; ++e) {  // rows past the end: dy = 0
+                    h[e] = mul2(add2(h[e], mu2), rs2);
+                    dw[i][e] = fma2(df[e], h[e], dw[i][e]);
+                    db[i][e] = add2(db[i][e], df[e]);
+                    df[e] = fma2(fma2(h[e], m2n, mul2(df[e], wf[i][e])), rs2, m1n);
+                }
+                if (row < p.rows && c < nvec) {
+                    typename V::P o;
+                    if constexpr (VW > 1) {
+                        o = V::pack2(df);
+                    } else {
+                        const float t[VW] = {up2(df[0]).x};
+                        o = V::pack(t);
+                    }
+                    V::store(dx + row * p.k + (int64_t)c * VW, o);
+                }
+            }
+        }
+    }
+    if (!p.part) return;
+    float *mine = p.part + part * p.part_cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = v0 + i * kColThreads;
+        if (c < nvec)
+#pragma unroll
+            for (int e = 0; e < VW; ++e) {
+                const float2 a = up2(dw[i][e / 2]), b = up2(db[i][e / 2]);
+                mine[c * VW + e] = e & 1 ? a.y : a.x;
+                if (!p.rms) mine[p.k + c * VW + e] = e & 1 ? b.y : b.x;
+            }
+    }
+}
+
+// dw and db: column sums of the partial rows. A CTA takes 32 columns; each of
+// its W warps adds every W-th partial row, then the W sums are added in order.
+template <int W>
+__global__ void __launch_bounds__(32 * W) norm_bwd_reduce_kernel(const float *part, int parts, int64_t cols, int k, float *dw,
+                                                                 float *db) {
+    __shared__ float sum[W][32];
     griddep_wait();
     griddep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;  // column of [dw | db]
     float s = 0.0f;
     if (c < cols) {
-#pragma unroll 4
-        for (int r = warp; r < parts; r += 32) s += part[r * cols + c];
+#pragma unroll 8
+        for (int r = warp; r < parts; r += W) s += part[r * cols + c];
     }
     sum[warp][lane] = s;
     __syncthreads();
-    const float t = warp_sum(sum[lane][warp]);  // column blockIdx.x * 32 + warp
-    const int64_t o = (int64_t)blockIdx.x * 32 + warp;
-    if (lane == 0 && o < cols) {
-        if (o < k) {
-            if (dw) dw[o] = t;
-        } else if (db) {
-            db[o - k] = t;
-        }
+    if (warp != 0 || c >= cols) return;
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) t += sum[i][lane];
+    if (c < k) {
+        if (dw) dw[c] = t;
+    } else if (db) {
+        db[c - k] = t;
     }
 }
 
@@ -634,21 +748,13 @@ sharq_status launch_layer_norm(LaunchCtx &ctx, const void *x, int64_t rows, int6
     });
 }
 
-// CTAs of a row in the backward pass, threads of such a CTA, and how many of
-// them an SM holds.
-static int bwd_cluster(int64_t k) {
-    int c = 1;
-    while ((int64_t)c * kBwdThreads * kBwdCols < k) c *= 2;
-    return c;
-}
 static int bwd_lanes(int64_t k) {  // of a row in the warp form
     int l = 1;
     while (l * kBwdCols < k) l *= 2;
     return l;
 }
-static int bwd_threads(int64_t k, int cluster) {
-    return (int)round_up(((k + kBwdCols - 1) / kBwdCols + cluster - 1) / cluster, 32);
-}
+// Threads of a row's CTA, and how many such CTAs an SM holds.
+static int bwd_threads(int64_t k) { return (int)round_up((k + kBwdCols - 1) / kBwdCols, 32); }
 static int bwd_per_sm(int threads) {
     if (threads > kBwdSmall) return 1;
     const int n = 2 * kBwdSmall / threads;
@@ -658,15 +764,19 @@ static int bwd_per_sm(int threads) {
 // Row groups of the backward pass, each with a partial row of the weight
 // gradients (a workspace size, so a function of the shape alone). A group has
 // some rows to itself, or the partial rows outweigh the pass.
-int64_t norm_bwd_parts(int64_t rows, int64_t k) {
+static int64_t norm_bwd_parts(int64_t rows, int64_t k) {
     if (rows <= 0) return 0;
     const int64_t sms = 148;
     if (k <= 32 * kBwdCols) {
         const int64_t per = 32 * kBwdWarps / bwd_lanes(k), need = (rows + per - 1) / per;
         return need < 2 * sms ? need : 2 * sms;
     }
-    const int cluster = bwd_cluster(k);
-    const int64_t most = bwd_per_sm(bwd_threads(k, cluster)) * sms / cluster;
+    if (k > kBwdRow) {  // two CTAs per SM (as fit), each with at least kColRows rows
+        const int64_t across = (k + 2047) / 2048, most = across < 2 * sms ? 2 * sms / across : 1;
+        const int64_t need = (rows + kColRows - 1) / kColRows;
+        return need < most ? need : most;
+    }
+    const int64_t most = bwd_per_sm(bwd_threads(k)) * sms;
     const int64_t few = rows <= 64 ? rows : rows / 4 < 64 ? 64 : rows / 4;
     return few < most ? few : most;
 }
@@ -679,15 +789,21 @@ static sharq_status norm_bwd(LaunchCtx &ctx, const NormBwdParams &p) {
         const size_t smem = (size_t)(32 * kBwdWarps / q.lanes) * 2 * p.k * sizeof(float);  // at most 32 KB
         return launch_pdl(ctx, norm_bwd_kernel<T, VW, true>, p.parts, 32 * kBwdWarps, smem, 1, q);
     }
-    const int cluster = bwd_cluster(p.k), threads = bwd_threads(p.k, cluster);
+    if (p.k > kBwdRow) {
+        constexpr int NV = VW == 8 ? 1 : VW == 4 ? 2 : 4;
+        const sharq_status st = launch_pdl(ctx, norm_bwd_sums_kernel<T, VW>, p.rows, kBwdThreads, 0, 1, p);
+        if (st != SHARQ_OK) return st;
+        const int64_t across = (p.k / VW + kColThreads * NV - 1) / (kColThreads * NV);
+        return launch_pdl(ctx, norm_bwd_cols_kernel<T, VW, NV>, across * p.parts, kColThreads, 0, 1, p);
+    }
+    const int threads = bwd_threads(p.k);
     if constexpr (VW > 1) {
-        const int64_t pair = 2 * 16 * ((p.k / VW + cluster - 1) / cluster);
+        const int64_t pair = 2 * 16 * (p.k / VW);
         const int64_t fit = kRingBytes / bwd_per_sm(threads) / pair;
         const int stages = fit > kRingMax ? kRingMax : (int)fit;  // at least 2: a pair of rows has at most 64 KB
-        const bool full = p.k % ((int64_t)cluster * threads * kBwdCols) == 0;
+        const bool full = p.k % ((int64_t)threads * kBwdCols) == 0;
         auto run = [&](auto kernel) {
-            return launch_pdl(ctx, kernel, (int64_t)p.parts * cluster, threads, (size_t)(stages * pair), cluster, p, stages,
-                              ctx.wait_ns, ctx.status);
+            return launch_pdl(ctx, kernel, p.parts, threads, (size_t)(stages * pair), 1, p, stages, ctx.wait_ns, ctx.status);
         };
         SQ_SMEM_ONCE((norm_bwd_ring_kernel<T, VW, kBwdSmall, true>), kRingBytes);
         SQ_SMEM_ONCE((norm_bwd_ring_kernel<T, VW, kBwdSmall, false>), kRingBytes);
@@ -697,18 +813,27 @@ static sharq_status norm_bwd(LaunchCtx &ctx, const NormBwdParams &p) {
             return full ? run(norm_bwd_ring_kernel<T, VW, kBwdSmall, true>) : run(norm_bwd_ring_kernel<T, VW, kBwdSmall, false>);
         return full ? run(norm_bwd_ring_kernel<T, VW, kBwdThreads, true>) : run(norm_bwd_ring_kernel<T, VW, kBwdThreads, false>);
     } else {
-        return launch_pdl(ctx, norm_bwd_kernel<T, VW, false>, (int64_t)p.parts * cluster, threads, 0, cluster, p);
+        return launch_pdl(ctx, norm_bwd_kernel<T, VW, false>, p.parts, threads, 0, 1, p);
     }
 }
 
+int64_t norm_bwd_bytes(int64_t rows, int64_t k) {
+    return round_up(norm_bwd_parts(rows, k) * 2 * k * (int64_t)sizeof(float), kAlign) + (k > kBwdRow ? rows * 8 : 0);
+}
+
+bool norm_bwd_one_pass(int64_t k) { return k <= kBwdRow; }
+
 sharq_status launch_layer_norm_backward(LaunchCtx &ctx, const void *dy, const void *x, int64_t rows, int64_t k,
                                         const void *w, const float *mean, const float *rstd, int norm, int dtype,
-                                        void *dx, float *dw, float *db, float *part, bool vec16) {
+                                        void *dx, float *dw, float *db, void *ws, bool vec16) {
+    float *part = static_cast<float *>(ws);
     const int parts = (int)norm_bwd_parts(rows, k);
     const bool grads = dw || db;
     const int64_t cols = norm == 1 ? k : 2 * k;  // RMSNorm has no db
     if (rows > 0) {
-        NormBwdParams p{dy, x, w, mean, rstd, dx, grads ? part : nullptr, rows, cols, (int32_t)k, parts, norm, 32};
+        NormBwdParams p{dy, x, w, mean, rstd, dx, grads ? part : nullptr, rows, cols, (int32_t)k, parts, norm, 32, nullptr};
+        if (k > kBwdRow)
+            p.sums = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + round_up((int64_t)parts * 2 * k * (int64_t)sizeof(float), kAlign));
         const sharq_status st = with_dtype(dtype, [&](auto t) {
             using T = decltype(t);
             return vec16 ? norm_bwd<T, 16 / (int)sizeof(T)>(ctx, p) : norm_bwd<T, 1>(ctx, p);
@@ -716,7 +841,9 @@ sharq_status launch_layer_norm_backward(LaunchCtx &ctx, const void *dy, const vo
         if (st != SHARQ_OK) return st;
     }
     if (!grads) return SHARQ_OK;
-    return launch_pdl(ctx, norm_bwd_reduce_kernel, (cols + 31) / 32, 1024, 0, 1, (const float *)part, parts, cols, (int)k, dw, db);
+    const int64_t grid = (cols + 31) / 32;
+    return parts > 128 ? launch_pdl(ctx, norm_bwd_reduce_kernel<32>, grid, 1024, 0, 1, part, parts, cols, (int)k, dw, db)
+                       : launch_pdl(ctx, norm_bwd_reduce_kernel<8>, grid, 256, 0, 1, part, parts, cols, (int)k, dw, db);
 }
 
 }  // namespace sq

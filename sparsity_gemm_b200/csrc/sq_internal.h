@@ -50,11 +50,13 @@ sharq_status launch_div_check(LaunchCtx &ctx, uint64_t count, uint64_t seed, uin
 // buffers allow 16-byte accesses.
 sharq_status launch_layer_norm(LaunchCtx &ctx, const void *x, int64_t rows, int64_t k, const void *w, const void *b,
                                float eps, int norm, int dtype, void *y, float *mean, float *rstd, bool vec16);
-// Partial rows ([2][k] floats each) of the weight gradients.
-int64_t norm_bwd_parts(int64_t rows, int64_t k);
+// Workspace of the backward pass in bytes; needed for weight gradients, and
+// in any case where it takes more than one pass over a row.
+int64_t norm_bwd_bytes(int64_t rows, int64_t k);
+bool norm_bwd_one_pass(int64_t k);
 sharq_status launch_layer_norm_backward(LaunchCtx &ctx, const void *dy, const void *x, int64_t rows, int64_t k,
                                         const void *w, const float *mean, const float *rstd, int norm, int dtype,
-                                        void *dx, float *dw, float *db, float *part, bool vec16);
+                                        void *dx, float *dw, float *db, void *ws, bool vec16);
 sharq_status launch_route(LaunchCtx &ctx, const void *ids, int id_bytes, int64_t tokens, int64_t top_k, int64_t groups,
                           int32_t *offsets, int32_t *rows, int32_t *slots);
 sharq_status launch_permute(LaunchCtx &ctx, const void *x, int64_t tokens, int64_t k, const int32_t *slots, int64_t top_k,

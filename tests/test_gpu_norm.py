@@ -131,6 +131,14 @@ def test_without_affine_parameters(dt, with_w, with_b):
     _check_backward(dy, x, mean, rstd, w, "layer")
 
 
+@pytest.mark.parametrize("norm", ["layer", "rms"])
+def test_long_rows_without_weights(norm):
+    for k in (8200, 9001, 20000):
+        x, _, _, dy = _inputs(k, 9, k, torch.float16)
+        mean, rstd = _check_forward(x, None, None, 1e-5, norm)
+        _check_backward(dy, x, mean, rstd, None, norm)
+
+
 @pytest.mark.parametrize("dt", list(DTYPES))
 def test_buffers_that_miss_16_byte_alignment(dt):
     x, w, b, dy = _inputs(6, 21, 1024, DTYPES[dt], offset=1)

@@ -55,7 +55,8 @@ def test_layer_norm_backward_refusals(L):
 
     for bad in (dict(k=0), dict(k=65537), dict(m=-1), dict(dt=-1), dict(norm=1), dict(norm=0, mean=None), dict(rstd=None),
                 dict(dy=None), dict(x=None), dict(dx=None), dict(dx=P(2)), dict(dx=P(1, 2)), dict(dx=P(3)), dict(ws=None),
-                dict(ws=P(9, 128)), dict(n=need - 1), dict(dw=P(7, 2)), dict(db=P(7)), dict(db=P(7, 1020)), dict(x=P(2, 1))):
+                dict(ws=P(9, 128)), dict(n=need - 1), dict(dw=P(7, 2)), dict(db=P(7)), dict(db=P(7, 1020)), dict(x=P(2, 1)),
+                dict(k=9000, dw=None, db=None, ws=None, dx=P(10))):  # rows in two passes need the workspace in any case
         assert call(**bad) == sq.ERR_INVALID_ARG, bad
 
 
