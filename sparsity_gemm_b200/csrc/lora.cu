@@ -226,7 +226,7 @@ __device__ __forceinline__ void expand_tile(const LoraParams &p, int group, cons
     };
 #pragma unroll
     for (int s = 0; s < kAhead - 1; ++s) fetch(c0 + warp + s * kLoraWarps, s);
-    constexpr bool kNextB = NB == 2;  // more does not fit in registers
+    constexpr bool kNextB = NB == 2 || (MT == 1 && NB <= 8);  // more does not fit in registers
     uint4 bv[4][kS], bn[4][kS];
     if (kNextB) fetch_b(c0 + warp, bn);
     ready();
@@ -328,18 +328,19 @@ static int bare_ctas(const LaunchCtx &ctx, const LoraParams &p) {
     return (int)(n < ctx.num_sms ? n : ctx.num_sms);
 }
 
-// MT: 16-row blocks of a tile. NB: 8-column blocks of the padded rank.
-template <typename T, int MT, int NB>
+// NB: 8-column blocks of the padded rank.
+constexpr int kLoraCluster = 8;  // most CTAs of a tile
+template <int NB>
 struct LoraCfg {
-    static constexpr int kRows = 16 * MT, kRank = 8 * NB;
+    static constexpr int kRows = 16, kRank = 8 * NB;
     static constexpr int kLd = kRank + 8;   // row stride of the binary32 parts and of the 16-bit terms
-    static constexpr int kSmem = kLoraWarps * kRows * kLd * 4 + 2 * kRows * kLd * 2 + kAheadBytes<MT>;
+    static constexpr int kSmem = kLoraWarps * kRows * kLd * 4 + 2 * kRows * kLd * 2 + kAheadBytes<1>;
     static constexpr int kStep = NB >= 8 ? 1 : 2;  // steps of 32 elements of k in flight
 };
 
-template <typename T, int MT, int NB>
+template <typename T, int NB>
 __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraParams p) {
-    using C = LoraCfg<T, MT, NB>;
+    using C = LoraCfg<NB>;
     extern __shared__ __align__(16) uint8_t smem[];
     float *part = reinterpret_cast<float *>(smem);  // [warps][rows][kLd]; [0]: the CTA's sum
     uint16_t *hh = reinterpret_cast<uint16_t *>(smem + kLoraWarps * C::kRows * C::kLd * 4);  // [rows][kLd]
@@ -381,117 +382,111 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraParams p) 
         }
         __syncthreads();
 
-        // h = x A^T over this CTA's steps of k; warps take turns
+        // The columns' part of B and base set out first; h is made meanwhile.
         const T *a = static_cast<const T *>(p.a) + (int64_t)group * p.rank * p.k;
-        const T *xr[MT][2];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
+        auto make_h = [&]() {
+            // h = x A^T over this CTA's steps of k; warps take turns
+            const T *xr[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int32_t r = row_s[16 * i + 8 * h + g8];
-                xr[i][h] = r >= 0 ? static_cast<const T *>(p.x) + (int64_t)r * p.ldx : nullptr;
+                const int32_t r = row_s[8 * h + g8];
+                xr[h] = r >= 0 ? static_cast<const T *>(p.x) + (int64_t)r * p.ldx : nullptr;
             }
-        float acc[MT][NB][4];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
+            float acc[NB][4];
 #pragma unroll
             for (int j = 0; j < NB; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
-        const int steps = (p.k + 32 * C::kStep - 1) / (32 * C::kStep);
-        const int s0 = (int)((int64_t)steps * crank / csize), s1 = (int)((int64_t)steps * (crank + 1) / csize);
-        for (int s = s0 + warp; s < s1; s += kLoraWarps) {
-            uint4 xv[C::kStep][MT][2], av[C::kStep][NB];
+                for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+            const int steps = (p.k + 32 * C::kStep - 1) / (32 * C::kStep);
+            const int s0 = (int)((int64_t)steps * crank / csize), s1 = (int)((int64_t)steps * (crank + 1) / csize);
+            for (int s = s0 + warp; s < s1; s += kLoraWarps) {
+                uint4 xv[C::kStep][2], av[C::kStep][NB];
 #pragma unroll
-            for (int u = 0; u < C::kStep; ++u) {
-                const int kk = (s * C::kStep + u) * 32 + q * 8;
-                const bool in = kk < p.k;
-#pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    const int r = 8 * j + g8;
-                    av[u][j] = in && r < p.rank ? __ldg(reinterpret_cast<const uint4 *>(a + (int64_t)r * p.k + kk))
-                                                : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        xv[u][i][h] = in && xr[i][h] ? __ldg(reinterpret_cast<const uint4 *>(xr[i][h] + kk))
-                                                     : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int u = 0; u < C::kStep; ++u)
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
+                for (int u = 0; u < C::kStep; ++u) {
+                    const int kk = (s * C::kStep + u) * 32 + q * 8;
+                    const bool in = kk < p.k;
 #pragma unroll
                     for (int j = 0; j < NB; ++j) {
-                        const uint4 &x0 = xv[u][i][0], &x1 = xv[u][i][1], &b = av[u][j];
-                        mma16816(acc[i][j], x0.x, x1.x, x0.y, x1.y, b.x, b.y, T());
-                        mma16816(acc[i][j], x0.z, x1.z, x0.w, x1.w, b.z, b.w, T());
+                        const int r = 8 * j + g8;
+                        av[u][j] = in && r < p.rank ? __ldg(reinterpret_cast<const uint4 *>(a + (int64_t)r * p.k + kk))
+                                                    : make_uint4(0, 0, 0, 0);
                     }
-        }
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+                    for (int h = 0; h < 2; ++h)
+                        xv[u][h] = in && xr[h] ? __ldg(reinterpret_cast<const uint4 *>(xr[h] + kk)) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int u = 0; u < C::kStep; ++u)
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        const uint4 &x0 = xv[u][0], &x1 = xv[u][1], &b = av[u][j];
+                        mma16816(acc[j], x0.x, x1.x, x0.y, x1.y, b.x, b.y, T());
+                        mma16816(acc[j], x0.z, x1.z, x0.w, x1.w, b.z, b.w, T());
+                    }
+            }
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-                float *d = part + (warp * C::kRows + 16 * i + g8) * C::kLd + 8 * j + 2 * q;
-                *reinterpret_cast<float2 *>(d) = make_float2(acc[i][j][0], acc[i][j][1]);
-                *reinterpret_cast<float2 *>(d + 8 * C::kLd) = make_float2(acc[i][j][2], acc[i][j][3]);
+                float *d = part + (warp * C::kRows + g8) * C::kLd + 8 * j + 2 * q;
+                *reinterpret_cast<float2 *>(d) = make_float2(acc[j][0], acc[j][1]);
+                *reinterpret_cast<float2 *>(d + 8 * C::kLd) = make_float2(acc[j][2], acc[j][3]);
             }
-        __syncthreads();
-        for (int i = threadIdx.x; i < C::kRows * C::kRank; i += kLoraThreads) {
-            float *d = part + (i / C::kRank) * C::kLd + i % C::kRank;
-            float sum = d[0];
+            __syncthreads();
+            for (int i = threadIdx.x; i < count * C::kRank; i += kLoraThreads) {
+                float *d = part + (i / C::kRank) * C::kLd + i % C::kRank;
+                float sum = d[0];
 #pragma unroll
-            for (int w = 1; w < kLoraWarps; ++w) sum += d[w * C::kRows * C::kLd];
-            d[0] = sum;
-        }
-        if (csize > 1) cluster_sync();
-        else __syncthreads();
-        // every CTA adds the parts in rank order, so all hold the same h
-        const float scale = p.scales ? p.scales[group] : 1.0f;
-        for (int r = warp; r < C::kRows; r += kLoraWarps) {
-            constexpr int kPer = (C::kRank + 31) / 32;
-            float h[kPer], top = 0.0f;
+                for (int w = 1; w < kLoraWarps; ++w) sum += d[w * C::kRows * C::kLd];
+                d[0] = sum;
+            }
+            cluster_sync();
+            // every CTA adds the parts in rank order, so all hold the same h
+            const float scale = p.scales ? p.scales[group] : 1.0f;
+            for (int r = warp; r < count; r += kLoraWarps) {
+                constexpr int kPer = (C::kRank + 31) / 32;
+                float h[kPer], top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int c = i * 32 + lane;
-                h[i] = 0.0f;
-                if (c < C::kRank) {
-                    const uint32_t at = smem_u32(part + r * C::kLd + c);
-                    if (csize == 1) h[i] = part[r * C::kLd + c];
-                    else
-                        for (uint32_t z = 0; z < csize; ++z) h[i] += ld_cluster_f32(mapa_shared(at, z));
+                for (int i = 0; i < kPer; ++i) {
+                    const int c = i * 32 + lane;
+                    const uint32_t at = smem_u32(part + r * C::kLd + (c < C::kRank ? c : 0));
+                    float v[kLoraCluster];  // all in flight
+#pragma unroll
+                    for (uint32_t z = 0; z < kLoraCluster; ++z) v[z] = z < csize ? ld_cluster_f32(mapa_shared(at, z)) : 0.0f;
+                    h[i] = 0.0f;
+#pragma unroll
+                    for (uint32_t z = 0; z < kLoraCluster; ++z) h[i] += v[z];
+                    if (c >= C::kRank) h[i] = 0.0f;
+                    top = fmaxf(top, fabsf(h[i]));
                 }
-                top = fmaxf(top, fabsf(h[i]));
-            }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            // a power of two that brings the row's largest value to [1, 2)
-            int e = (int)(__float_as_uint(top) >> 23) - 127;
-            e = e < -100 ? -100 : e > 126 ? 0 : e;
-            const float down = pow2f(-e), up = pow2f(e);
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                // a power of two that brings the row's largest value to [1, 2)
+                int e = (int)(__float_as_uint(top) >> 23) - 127;
+                e = e < -100 ? -100 : e > 126 ? 0 : e;
+                const float down = pow2f(-e), up = pow2f(e);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int c = i * 32 + lane;
-                if (c < C::kRank) {
-                    const float v = h[i] * down;
-                    const T hi = narrow<T>(v);
-                    const T lo = narrow<T>(v - widen(hi));
-                    memcpy(hh + r * C::kLd + c, &hi, 2);
-                    memcpy(hl + r * C::kLd + c, &lo, 2);
+                for (int i = 0; i < kPer; ++i) {
+                    const int c = i * 32 + lane;
+                    if (c < C::kRank) {
+                        const float v = h[i] * down;
+                        const T hi = narrow<T>(v);
+                        const T lo = narrow<T>(v - widen(hi));
+                        memcpy(hh + r * C::kLd + c, &hi, 2);
+                        memcpy(hl + r * C::kLd + c, &lo, 2);
+                    }
                 }
+                if (lane == 0) scale_s[r] = scale * up;
             }
-            if (lane == 0) scale_s[r] = scale * up;
-        }
-        __syncthreads();
+            __syncwarp();
+            cluster_arrive_relaxed();  // this CTA reads no other CTA's part any more
+            __syncthreads();
+        };
 
         const int64_t piece = (int64_t)part_n * csize + crank, pieces = (int64_t)p.nsplit * csize;
         const int blocks = (p.n + 31) / 32;
-        expand_tile<T, MT, NB>(p, group, row_s, scale_s, hh, hl, smem + C::kSmem - kAheadBytes<MT>,
-                               (int)(blocks * piece / pieces), (int)(blocks * (piece + 1) / pieces), []() {});
+        expand_tile<T, 1, NB>(p, group, row_s, scale_s, hh, hl, smem + C::kSmem - kAheadBytes<1>,
+                               (int)(blocks * piece / pieces), (int)(blocks * (piece + 1) / pieces), make_h);
+        cluster_wait();  // no CTA leaves while another reads its part
     }
-    if (group >= 0 && csize > 1) cluster_sync();  // no CTA leaves while another reads its part
 }
 
 // ---------------------------------------------------------------------------
@@ -657,12 +652,16 @@ __global__ void __launch_bounds__(kShThreads)
         float *own = part + row * C::kLd;  // this row's part here is only read by its own threads from now on
         for (int c = sub; c < kGroups; c += (int)csize) {
             float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (uint32_t z = 0; z < csize; ++z) {  // in rank order
-                const float4 v = ld_cluster_f4(mapa_shared(smem_u32(own + 4 * c), z));
-                a.x += v.x;
-                a.y += v.y;
-                a.z += v.z;
-                a.w += v.w;
+            float4 v[kLoraCluster];  // all in flight
+#pragma unroll
+            for (uint32_t z = 0; z < kLoraCluster; ++z)
+                v[z] = z < csize ? ld_cluster_f4(mapa_shared(smem_u32(own + 4 * c), z)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int z = 0; z < kLoraCluster; ++z) {  // added in rank order
+                a.x += v[z].x;
+                a.y += v[z].y;
+                a.z += v[z].z;
+                a.w += v[z].w;
             }
             // the columns behind the rank belong to another adapter
             if (4 * c >= p.rank) a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -786,7 +785,7 @@ static sharq_status lora_two(LaunchCtx &ctx, LoraParams p) {
     // Splits of k: until the tiles would take more than 3 CTAs per SM (two fit;
     // the bound on the tiles is rarely met)
     int cluster = 1;
-    while (cluster < 8 && tiles * cluster * 2 <= 3 * ctx.num_sms && p.k >= 2 * kShK * cluster) cluster *= 2;
+    while (cluster < kLoraCluster && tiles * cluster * 2 <= 3 * ctx.num_sms && p.k >= 2 * kShK * cluster) cluster *= 2;
     sharq_status st = launch_pdl(ctx, lora_shrink_kernel<T, R>, tiles * cluster, kShThreads, C::kSmem, cluster, tm_a, p);
     if (st != SHARQ_OK) return st;
     // CTAs that stay, unless that leaves a warp less than a block
@@ -807,19 +806,19 @@ int64_t lora_ws_bytes(int64_t m, int64_t rank, int64_t groups) {
     return round_up(m * 4 * shrink_rank(rank), kAlign) + round_up(m * 4, kAlign);
 }
 
-template <typename T, int MT, int NB>
+template <typename T, int NB>
 static sharq_status lora_run(LaunchCtx &ctx, LoraParams p) {
-    using C = LoraCfg<T, MT, NB>;
-    SQ_SMEM_ONCE((lora_kernel<T, MT, NB>), C::kSmem);
+    using C = LoraCfg<NB>;
+    SQ_SMEM_ONCE((lora_kernel<T, NB>), C::kSmem);
     const int64_t tiles = tiles_bound(p, C::kRows);
     // Split a tile until the CTAs fill the GPU twice, as long as a CTA keeps
     // a few hundred elements of k and of the columns.
     int cluster = 1;
-    while (cluster < 8 && tiles * cluster < 2 * ctx.num_sms && p.k >= 512 * cluster) cluster *= 2;
+    while (cluster < kLoraCluster && tiles * cluster < 2 * ctx.num_sms && p.k >= 512 * cluster) cluster *= 2;
     p.nsplit = 1;
-    while (p.nsplit < 16 && tiles * cluster * p.nsplit < ctx.num_sms && p.n >= 512 * cluster * p.nsplit) p.nsplit *= 2;
+    while (p.nsplit < 16 && tiles * cluster * p.nsplit < ctx.num_sms && p.n >= 256 * cluster * p.nsplit) p.nsplit *= 2;
     p.bare_ctas = (int32_t)round_up(bare_ctas(ctx, p), cluster);
-    return launch_pdl(ctx, lora_kernel<T, MT, NB>, p.bare_ctas + tiles * cluster * p.nsplit, kLoraThreads, C::kSmem, cluster, p);
+    return launch_pdl(ctx, lora_kernel<T, NB>, p.bare_ctas + tiles * cluster * p.nsplit, kLoraThreads, C::kSmem, cluster, p);
 }
 
 template <typename T>
@@ -832,10 +831,10 @@ static sharq_status lora_any(LaunchCtx &ctx, const LoraParams &p) {
             default: return lora_two<T, 16>(ctx, p);
         }
     }
-    if (p.rank <= 16) return lora_run<T, 1, 2>(ctx, p);
-    if (p.rank <= 32) return lora_run<T, 1, 4>(ctx, p);
-    if (p.rank <= 64) return lora_run<T, 1, 8>(ctx, p);
-    return lora_run<T, 1, 16>(ctx, p);
+    if (p.rank <= 16) return lora_run<T, 2>(ctx, p);
+    if (p.rank <= 32) return lora_run<T, 4>(ctx, p);
+    if (p.rank <= 64) return lora_run<T, 8>(ctx, p);
+    return lora_run<T, 16>(ctx, p);
 }
 
 sharq_status launch_lora(LaunchCtx &ctx, const void *x, int64_t ldx, int64_t m, int64_t k, const void *a, const void *b,
