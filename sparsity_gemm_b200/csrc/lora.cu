@@ -43,7 +43,7 @@ struct LoraParams {
     int32_t ldx, ldbase, ldo;
     int64_t m;
     int32_t k, n, rank, groups;
-    int32_t nsplit;  // clusters (expand: CTAs) that share a tile, each with its part of the columns
+    int32_t nsplit;     // one launch: clusters that share a tile, each with its part of the columns
     int32_t bare_ctas;  // CTAs, the grid's first, that copy rows without a group
     unsigned *status;
     uint64_t wait_ns;
@@ -291,9 +291,9 @@ __device__ __forceinline__ void expand_tile(const LoraParams &p, int group, cons
 }
 
 // Rows without a group: base (or zero), unless they are there already; the
-// grid's first p.bare_ctas CTAs do it, a row per warp. Rows
-// without a group come in runs (a request's rows), so the warps take rows in
-// turn; a warp looks at 32 of its rows at a time.
+// grid's first p.bare_ctas CTAs do it, a row per warp. Such rows come in runs (a
+// request's rows), so the warps take rows in turn; a warp looks at 32 of its
+// rows at a time.
 template <typename T>
 __device__ __forceinline__ void copy_bare_rows(const LoraParams &p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -494,13 +494,13 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraParams p) 
 //
 // The first computes h = x A^T on the tensor cores of the fifth generation:
 // 128 rows of a group per tile, gathered from x in 16-byte copies (a TMA gather
-// of four rows per copy measured 34 us against 24 for 8192 x 4096, rank 16), A's rows
-// beside them, k in steps of 64 through a ring of shared-memory stages, the
-// accumulator in tensor memory. The CTAs of a cluster split k and add their
+// of four rows per copy measured 34 us against 24 for 8192 x 4096, rank 16),
+// A's rows beside them, k in steps of 64 through a ring of shared-memory
+// stages, the accumulator in tensor memory. The CTAs of a cluster split k and add their
 // parts through distributed shared memory; h leaves as its two 16-bit terms.
-// It is bound by reading x. The second is the one-launch form's second
-// half on tiles of 32 rows, bound by base and out. Two launches keep both streaming
-// all the time; in one, a tile's reads of x and its writes alternate.
+// It is bound by reading x. The second is the one-launch form's second half on
+// tiles of 32 rows, bound by base and out. Two launches keep both streaming all
+// the time; in one, a tile's reads of x and its writes alternate.
 constexpr int kShRows = 128;
 constexpr int kShK = 64;
 constexpr int kShThreads = 192;  // warps 0-3: copies of x, then the accumulator; 4: copies of A; 5: products
@@ -510,7 +510,7 @@ constexpr int kShX = kShRows * kShK * 2;
 template <int R>
 struct ShrinkCfg {
     static constexpr int kStage = kShX + R * kShK * 2;
-    static constexpr int kStages = (R <= 64 ? 72 : 100) * 1024 / kStage;  // two CTAs on an SM
+    static constexpr int kStages = (R <= 64 ? 72 : 100) * 1024 / kStage;  // three CTAs on an SM (rank 128: two)
     static constexpr int kLd = R + 4;                    // row stride of the binary32 parts
     static constexpr int kPart = kShRows * kLd * 4;
     static constexpr int kSmem = 1024 + (kStages * kStage > kPart ? kStages * kStage : kPart);
@@ -521,14 +521,14 @@ struct ShrinkCfg {
 SQ_HD int shrink_rank(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
 template <typename T, int R>
-__global__ void __launch_bounds__(kShThreads)
+__global__ void __launch_bounds__(kShThreads, 2)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap tm_a, const LoraParams p) {
     using C = ShrinkCfg<R>;
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], done;
     __shared__ uint32_t tmem_s;
-    __shared__ int32_t off[kGroupsMax + 1];
-    __shared__ int32_t tile_s[3];
+    __shared__ int32_t off[kGroupsMax + 1], tiles[kGroupsMax + 1];
+    __shared__ int table_ok;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
     float *part = reinterpret_cast<float *>(dyn + (ring - smem_u32(dyn)));
@@ -550,146 +550,177 @@ __global__ void __launch_bounds__(kShThreads)
     uint32_t csize;
     asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
     const uint32_t crank = cluster_ctarank();
-    cta_find_tile(p, off, kShRows, (int)(blockIdx.x / csize), tile_s);  // its barrier also publishes the set-up above
+    for (int i = threadIdx.x; i <= p.groups; i += kShThreads) off[i] = p.offsets[i];
+    __syncthreads();  // also publishes the set-up above
     tc_fence_after();
-    const int group = tile_s[0], first = tile_s[1], count = tile_s[2];
-    if (group < 0) {  // the same for the whole cluster
-        if (warp == 5) tmem_dealloc(tmem_s, C::kTmem);
-        if (group == -2 && blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, kSiteBadOffsets);
+    if (warp == 0) {
+        const bool ok = build_tiles(off, p.groups, p.m, kShRows, tiles);
+        if (lane == 0) table_ok = ok;
+    }
+    __syncthreads();
+    const uint32_t tmem = tmem_s;
+    if (!table_ok) {  // the same for every CTA
+        if (blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, kSiteBadOffsets);
+        if (warp == 5) tmem_dealloc(tmem, C::kTmem);
         return;
     }
-    const uint32_t tmem = tmem_s;
+    // How many CTAs share a tile: as many of a cluster as the tiles there are
+    // leave to each (the launch knows only how many adapters there are, not how
+    // many of them the batch uses).
+    const int total = tiles[p.groups], ctas = (int)gridDim.x;
+    int split = (int)csize;
+    while (split > 1 && (int64_t)total * split > ctas) split /= 2;
+    const uint32_t sub_rank = crank % split, lead = crank - sub_rank;
+    const int units = ctas / split, unit = (int)blockIdx.x / split;
     const int blocks = (p.k + kShK - 1) / kShK;
-    const int b0 = (int)((int64_t)blocks * crank / csize), b1 = (int)((int64_t)blocks * (crank + 1) / csize);
-
-    if (warp < 4) {
-        // 16-byte copies into the products' layout (128-byte rows, piece c of
-        // row r at c ^ (r % 8)): 8 threads per row, every 16th row. Rows past
-        // the tile's end are not copied: what their lanes of the accumulator
-        // hold is not read.
-        const int r0 = threadIdx.x >> 3, piece = threadIdx.x & 7;
-        const T *src[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            src[j] = nullptr;
-            if (r0 + 16 * j < count) {
-                const int32_t v = p.rows[first + r0 + 16 * j];
-                // an invalid row is reported, and left out, by the second launch
-                src[j] = static_cast<const T *>(p.x) + (int64_t)(v >= 0 && v < p.m ? v : 0) * p.ldx + piece * 8;
-            }
+    const int b0 = (int)((int64_t)blocks * sub_rank / split), b1 = (int)((int64_t)blocks * (sub_rank + 1) / split);
+    int used = 0;  // ring stages used by the tiles before
+    uint32_t done_phase = 0;
+    // every CTA of a cluster takes as many steps: they meet in its barriers
+    for (int step = 0; step * units < total; ++step, done_phase ^= 1) {
+        const int tile = step * units + unit;
+        if (tile >= total) {
+            cluster_sync();
+            cluster_sync();
+            continue;
         }
-        const uint32_t at = (uint32_t)(r0 * 128 + ((piece ^ (r0 & 7)) * 16));  // rows 16 apart: the same r % 8
-        for (int b = b0; b < b1; ++b) {
-            const int i = b - b0, s = i % C::kStages;
-            const bool ok = mbar_wait_own(smem_u32(&empty[s]), ((i / C::kStages) & 1) ^ 1, p.status, kSiteLoraEmpty, p.wait_ns);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            const uint32_t dst = ring + s * C::kStage + at, in = b * kShK + piece * 8 < p.k ? 16u : 0u;
+        const int group = group_of_tile(tiles, p.groups, tile);
+        const int first = off[group] + (tile - tiles[group]) * kShRows, count = min(kShRows, off[group + 1] - first);
+        if (warp < 4) {
+            // 16-byte copies into the products' layout (128-byte rows, piece c of
+            // row r at c ^ (r % 8)): 8 threads per row, every 16th row. Rows past
+            // the tile's end are not copied: what their lanes of the accumulator
+            // hold is not read.
+            const int r0 = threadIdx.x >> 3, piece = threadIdx.x & 7;
+            const T *src[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (src[j]) cp_async16_zfill(dst + j * 16 * 128, in ? src[j] + b * kShK : src[j], in);
-            cp_async_arrive(smem_u32(&full[s]));
-        }
-    } else if (warp == 4) {
-        if (lane == 0) {
-            for (int b = b0; b < b1; ++b) {
-                const int i = b - b0, s = i % C::kStages;
-                if (!mbar_wait_own(smem_u32(&empty[s]), ((i / C::kStages) & 1) ^ 1, p.status, kSiteLoraEmpty, p.wait_ns)) break;
-                const uint32_t bar = smem_u32(&full[s]);
-                mbar_arrive_expect_tx(bar, R * kShK * 2);
-                tma_load_2d(ring + s * C::kStage + kShX, &tm_a, b * kShK, group * p.rank, bar);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 5) {
-        if (lane == 0) {
-            // D binary32; A and B of type T, both K-major; N = R, M = 128
-            const uint32_t fmt = IsBf16<T>::v ? 1u : 0u;
-            const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(R >> 3) << 17) | ((kShRows >> 4) << 24);
-            for (int b = b0; b < b1; ++b) {
-                const int i = b - b0, s = i % C::kStages;
-                if (!mbar_wait_own(smem_u32(&full[s]), (i / C::kStages) & 1, p.status, kSiteLoraFull, p.wait_ns)) break;
-                fence_proxy_async();  // x came through the generic proxy
-                tc_fence_after();
-                const uint32_t st = ring + s * C::kStage;
-                const uint64_t dx = smem_desc(st, 16, 8 * kShK * 2, 2u), da = smem_desc(st + kShX, 16, 8 * kShK * 2, 2u);
-#pragma unroll
-                for (int j = 0; j < kShK / 16; ++j) tc_mma_f16(tmem, dx + 2 * j, da + 2 * j, idesc, i != 0 || j != 0);
-                tc_commit(smem_u32(&empty[s]));
-            }
-            tc_commit(smem_u32(&done));
-        }
-        __syncwarp();
-    }
-    // Every thread waits for the products: the ring is free then, and the
-    // parts of h take its place.
-    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_own(smem_u32(&done), 0, p.status, kSiteLoraDone, p.wait_ns));
-    tc_fence_after();
-    if (warp < 4) {
-        float *row = part + (warp * 32 + lane) * C::kLd;
-#pragma unroll
-        for (int c = 0; c < R; c += 16) {
-            uint32_t v[16];
-            tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<float4 *>(row + c + e) =
-                    make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-        }
-    }
-    tc_fence_before();
-    cluster_sync();
-    if (warp == 5) {
-        tc_fence_after();
-        tmem_dealloc(tmem, C::kTmem);
-    }
-    if (warp < 4 && ok) {
-        // csize threads per row, each with every csize-th group of 4 columns
-        const int per = kShRows / (int)csize, mine = (int)threadIdx.x / (int)csize, sub = (int)threadIdx.x % (int)csize;
-        const int row = (int)crank * per + mine;
-        constexpr int kGroups = R / 4;
-        float top = 0.0f;
-        float *own = part + row * C::kLd;  // this row's part here is only read by its own threads from now on
-        for (int c = sub; c < kGroups; c += (int)csize) {
-            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            float4 v[kLoraCluster];  // all in flight
-#pragma unroll
-            for (uint32_t z = 0; z < kLoraCluster; ++z)
-                v[z] = z < csize ? ld_cluster_f4(mapa_shared(smem_u32(own + 4 * c), z)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int z = 0; z < kLoraCluster; ++z) {  // added in rank order
-                a.x += v[z].x;
-                a.y += v[z].y;
-                a.z += v[z].z;
-                a.w += v[z].w;
-            }
-            // the columns behind the rank belong to another adapter
-            if (4 * c >= p.rank) a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            *reinterpret_cast<float4 *>(own + 4 * c) = a;
-            top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(a.z), fabsf(a.w)));
-        }
-        for (int o = 1; o < (int)csize; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        int e = (int)(__float_as_uint(top) >> 23) - 127;
-        e = e < -100 ? -100 : e > 126 ? 0 : e;
-        const float down = pow2f(-e);
-        if (row < count) {
-            T *h = static_cast<T *>(p.h) + (int64_t)(first + row) * 2 * R;
-            for (int c = sub; c < kGroups; c += (int)csize) {
-                const float4 a = *reinterpret_cast<const float4 *>(own + 4 * c);
-                const float v[4] = {a.x * down, a.y * down, a.z * down, a.w * down};
-                T hi[4], lo[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    hi[j] = narrow<T>(v[j]);
-                    lo[j] = narrow<T>(v[j] - widen(hi[j]));
+            for (int j = 0; j < 8; ++j) {
+                src[j] = nullptr;
+                if (r0 + 16 * j < count) {
+                    const int32_t v = p.rows[first + r0 + 16 * j];
+                    // an invalid row is reported, and left out, by the second launch
+                    src[j] = static_cast<const T *>(p.x) + (int64_t)(v >= 0 && v < p.m ? v : 0) * p.ldx + piece * 8;
                 }
-                memcpy(h + 4 * c, hi, 8);
-                memcpy(h + R + 4 * c, lo, 8);
             }
-            if (sub == 0) p.hscale[first + row] = pow2f(e);
+            const uint32_t at = (uint32_t)(r0 * 128 + ((piece ^ (r0 & 7)) * 16));  // rows 16 apart: the same r % 8
+            for (int b = b0; b < b1; ++b) {
+                const int i = used + b - b0, s = i % C::kStages;
+                const bool ok = mbar_wait_own(smem_u32(&empty[s]), ((i / C::kStages) & 1) ^ 1, p.status, kSiteLoraEmpty, p.wait_ns);
+                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                const uint32_t dst = ring + s * C::kStage + at, in = b * kShK + piece * 8 < p.k ? 16u : 0u;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (src[j]) cp_async16_zfill(dst + j * 16 * 128, in ? src[j] + b * kShK : src[j], in);
+                cp_async_arrive(smem_u32(&full[s]));
+            }
+            cp_async_wait<0>();
+        } else if (warp == 4) {
+            if (lane == 0) {
+                for (int b = b0; b < b1; ++b) {
+                    const int i = used + b - b0, s = i % C::kStages;
+                    if (!mbar_wait_own(smem_u32(&empty[s]), ((i / C::kStages) & 1) ^ 1, p.status, kSiteLoraEmpty, p.wait_ns)) {
+                        // gave up: let the copies in flight land before the CTA's shared memory goes
+                        for (int f = i < C::kStages ? 0 : i - C::kStages; f < i; ++f)
+                            (void)mbar_wait_own(smem_u32(&full[f % C::kStages]), (f / C::kStages) & 1, nullptr, 0, 10000000ull);
+                        break;
+                    }
+                    const uint32_t bar = smem_u32(&full[s]);
+                    mbar_arrive_expect_tx(bar, R * kShK * 2);
+                    tma_load_2d(ring + s * C::kStage + kShX, &tm_a, b * kShK, group * p.rank, bar);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 5) {
+            if (lane == 0) {
+                // D binary32; A and B of type T, both K-major; N = R, M = 128
+                const uint32_t fmt = IsBf16<T>::v ? 1u : 0u;
+                const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(R >> 3) << 17) | ((kShRows >> 4) << 24);
+                for (int b = b0; b < b1; ++b) {
+                    const int i = used + b - b0, s = i % C::kStages;
+                    if (!mbar_wait_own(smem_u32(&full[s]), (i / C::kStages) & 1, p.status, kSiteLoraFull, p.wait_ns)) break;
+                    fence_proxy_async();  // x came through the generic proxy
+                    tc_fence_after();
+                    const uint32_t st = ring + s * C::kStage;
+                    const uint64_t dx = smem_desc(st, 16, 8 * kShK * 2, 2u), da = smem_desc(st + kShX, 16, 8 * kShK * 2, 2u);
+#pragma unroll
+                    for (int j = 0; j < kShK / 16; ++j) tc_mma_f16(tmem, dx + 2 * j, da + 2 * j, idesc, b != b0 || j != 0);
+                    tc_commit(smem_u32(&empty[s]));
+                }
+                tc_commit(smem_u32(&done));
+            }
+            __syncwarp();
         }
+        // Every thread waits for the products: the ring is free then, and the
+        // parts of h take its place.
+        const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_own(smem_u32(&done), done_phase, p.status, kSiteLoraDone, p.wait_ns));
+        tc_fence_after();
+        if (warp < 4) {
+            float *row = part + (warp * 32 + lane) * C::kLd;
+#pragma unroll
+            for (int c = 0; c < R; c += 16) {
+                uint32_t v[16];
+                tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    *reinterpret_cast<float4 *>(row + c + e) =
+                        make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+            }
+        }
+        tc_fence_before();
+        cluster_sync();
+        tc_fence_after();  // the next tile's products overwrite the accumulator
+        if (warp < 4 && ok) {
+            // split threads per row, each with every split-th group of 4 columns
+            const int per = kShRows / split, mine = (int)threadIdx.x / split, sub = (int)threadIdx.x % split;
+            const int row = (int)sub_rank * per + mine;
+            constexpr int kGroups = R / 4;
+            float top = 0.0f;
+            float *own = part + row * C::kLd;  // this row's part here is only read by its own threads from now on
+            for (int c = sub; c < kGroups; c += split) {
+                float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float4 v[kLoraCluster];  // all in flight
+#pragma unroll
+                for (uint32_t z = 0; z < kLoraCluster; ++z)
+                    v[z] = z < (uint32_t)split ? ld_cluster_f4(mapa_shared(smem_u32(own + 4 * c), lead + z)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int z = 0; z < kLoraCluster; ++z) {  // added in rank order
+                    a.x += v[z].x;
+                    a.y += v[z].y;
+                    a.z += v[z].z;
+                    a.w += v[z].w;
+                }
+                // the columns behind the rank belong to another adapter
+                if (4 * c >= p.rank) a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                *reinterpret_cast<float4 *>(own + 4 * c) = a;
+                top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(a.z), fabsf(a.w)));
+            }
+            for (int o = 1; o < split; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            int e = (int)(__float_as_uint(top) >> 23) - 127;
+            e = e < -100 ? -100 : e > 126 ? 0 : e;
+            const float down = pow2f(-e);
+            if (row < count) {
+                T *h = static_cast<T *>(p.h) + (int64_t)(first + row) * 2 * R;
+                for (int c = sub; c < kGroups; c += split) {
+                    const float4 a = *reinterpret_cast<const float4 *>(own + 4 * c);
+                    const float v[4] = {a.x * down, a.y * down, a.z * down, a.w * down};
+                    T hi[4], lo[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        hi[j] = narrow<T>(v[j]);
+                        lo[j] = narrow<T>(v[j] - widen(hi[j]));
+                    }
+                    memcpy(h + 4 * c, hi, 8);
+                    memcpy(h + R + 4 * c, lo, 8);
+                }
+                if (sub == 0) p.hscale[first + row] = pow2f(e);
+            }
+        }
+        fence_proxy_async();  // the next tile's copies overwrite the parts
+        cluster_sync();       // once no other CTA reads this one's
+        used += b1 - b0;
     }
-    cluster_sync();  // no CTA leaves while another reads its part
+    if (warp == 5) tmem_dealloc(tmem, C::kTmem);
 }
 
 // Tiles of 32 rows: 64 rows halve what is read of B (from L2) but leave two
@@ -699,7 +730,6 @@ __global__ void __launch_bounds__(kShThreads)
 constexpr int kExRows = 32;
 template <int NB>
 constexpr int kExPerSm = NB <= 4 ? 3 : 2;
-
 
 // The tiles' blocks of 32 columns, laid end to end, are divided evenly among
 // the CTAs, which stay for the whole launch: a CTA's share ends inside a tile.
@@ -781,12 +811,15 @@ static sharq_status lora_two(LaunchCtx &ctx, LoraParams p) {
     if (!make_row_map(&tm_a, p.a, (uint64_t)p.k, (uint64_t)p.groups * p.rank, (uint64_t)p.k * 2, R))
         return SHARQ_ERR_CUDA;
     SQ_SMEM_ONCE((lora_shrink_kernel<T, R>), C::kSmem);
-    const int64_t tiles = tiles_bound(p, kShRows);
-    // Splits of k: until the tiles would take more than 3 CTAs per SM (two fit;
-    // the bound on the tiles is rarely met)
+    // Clusters that stay and take tiles in turn, three CTAs to an SM; their size
+    // as if every tile were full (the kernel splits a tile less where there are
+    // more).
+    const int64_t full = (p.m + kShRows - 1) / kShRows;
     int cluster = 1;
-    while (cluster < kLoraCluster && tiles * cluster * 2 <= 3 * ctx.num_sms && p.k >= 2 * kShK * cluster) cluster *= 2;
-    sharq_status st = launch_pdl(ctx, lora_shrink_kernel<T, R>, tiles * cluster, kShThreads, C::kSmem, cluster, tm_a, p);
+    while (cluster < kLoraCluster && full * cluster * 2 <= 3 * ctx.num_sms && p.k >= 2 * kShK * cluster) cluster *= 2;
+    const int64_t tiles = tiles_bound(p, kShRows), fit = 3 * ctx.num_sms / cluster;
+    sharq_status st = launch_pdl(ctx, lora_shrink_kernel<T, R>, (tiles < fit ? tiles : fit) * cluster, kShThreads, C::kSmem,
+                                 cluster, tm_a, p);
     if (st != SHARQ_OK) return st;
     // CTAs that stay, unless that leaves a warp less than a block
     const int64_t ex = tiles_bound(p, kExRows) * ((p.n + 32 * kLoraWarps - 1) / (32 * kLoraWarps));
@@ -797,12 +830,21 @@ static sharq_status lora_two(LaunchCtx &ctx, LoraParams p) {
     return launch_pdl(ctx, lora_expand_kernel<T, NB>, ctas, kLoraThreads, kAheadBytes<kExRows / 16>, 1, p);
 }
 
-// Whether a call takes the two-launch form (and so needs a workspace): rows
-// of an adapter, on average, beyond what a 16-row tile holds.
-static bool lora_many(int64_t m, int64_t groups) { return m > 16 * groups; }
+// Whether a call takes the two-launch form (and so needs a workspace), by what
+// the host knows: rows, rank and adapters (not how many of them the batch
+// uses). Measured at k = n = 4096 in fp16, one launch against two, in us:
+//   rank 16   1 adapter:   512 rows  9.5 / 12.2, 1024 16.7 / 16.1, 4096 37 / 31
+//             64 adapters: 1024     13.3 / 25.1, 4096 37 / 39
+//   rank 64   1 adapter:   16 rows  7.8 / 12.3, 64 14.4 / 12.6, 1024 42 / 21
+//             64 adapters: 512      25 / 34, 1024 31 / 37, 4096 77 / 59
+// A 16-row tile's accumulators and its reading of A and B per 16 rows cost the
+// one-launch form more the larger the rank is.
+static bool lora_many(int64_t m, int64_t rank, int64_t groups) {
+    return rank <= 32 ? m >= 1024 && m > 32 * groups : m >= 64 && m >= 16 * groups;
+}
 
 int64_t lora_ws_bytes(int64_t m, int64_t rank, int64_t groups) {
-    if (!lora_many(m, groups)) return 0;
+    if (!lora_many(m, rank, groups)) return 0;
     return round_up(m * 4 * shrink_rank(rank), kAlign) + round_up(m * 4, kAlign);
 }
 
@@ -823,7 +865,7 @@ static sharq_status lora_run(LaunchCtx &ctx, LoraParams p) {
 
 template <typename T>
 static sharq_status lora_any(LaunchCtx &ctx, const LoraParams &p) {
-    if (lora_many(p.m, p.groups)) {
+    if (lora_many(p.m, p.rank, p.groups)) {
         switch (shrink_rank(p.rank)) {
             case 16: return lora_two<T, 2>(ctx, p);
             case 32: return lora_two<T, 4>(ctx, p);

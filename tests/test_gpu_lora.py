@@ -72,13 +72,23 @@ SHAPES = [(1, 256, 256, 16, 1), (1, 4096, 14336, 64, 3), (2, 8, 8, 8, 1), (5, 26
           (64, 512, 768, 16, 32), (17, 768, 1000, 32, 1), (33, 520, 328, 40, 1), (63, 256, 264, 16, 1), (64, 256, 256, 16, 1),
           (65, 256, 256, 16, 1), (129, 304, 96, 48, 2), (300, 512, 512, 64, 3), (300, 512, 520, 72, 3), (200, 640, 640, 128, 2),
           (40, 640, 640, 120, 40), (1000, 256, 512, 16, 1), (1000, 384, 320, 32, 7), (777, 512, 256, 64, 100),
-          (500, 256, 256, 8, 1024), (4099, 256, 264, 56, 5)]
+          (500, 256, 256, 8, 1024), (4099, 256, 264, 56, 5), (1100, 256, 264, 16, 2), (2100, 328, 512, 32, 5),
+          (1500, 136, 200, 8, 1), (64, 4096, 256, 96, 1), (70000, 64, 32, 64, 3), (20000, 72, 40, 40, 1000)]
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("m,k,n,rank,groups", SHAPES)
 def test_adapters(m, k, n, rank, groups, dt):
     c = _case(m + k + rank, m, k, n, rank, groups, DTYPES[dt])
+    _check(c, _run(c))
+
+
+@pytest.mark.parametrize("m,rank,groups", [(300, 16, 700), (8100, 64, 500), (8100, 64, 40), (4000, 16, 100)])
+def test_many_adapters_few_of_them_used(m, rank, groups):
+    """As a server has them: hundreds loaded, two in the batch (the launch
+    knows only how many are loaded)."""
+    c = _case(m + groups, m, 264, 72, rank, groups, torch.bfloat16)
+    c["ids"] = torch.where(c["ids"] % 3 == 0, groups - 1, torch.where(c["ids"] >= 0, 3, c["ids"])).int()
     _check(c, _run(c))
 
 
