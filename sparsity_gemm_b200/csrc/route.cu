@@ -223,13 +223,13 @@ sharq_status launch_route(LaunchCtx &ctx, const void *ids, int id_bytes, int64_t
 }
 
 // ---------------------------------------------------------------------------
-// Rows into grouped order and back. One CTA per token: the token's own row is
-// read (or written) once, its top_k grouped rows are touched with all their
-// loads in flight. Rows of the grouped matrix behind the last group's are
-// zero in permute's and the gradient's outputs; they are spread over the
-// CTAs.
+// Rows into grouped order and back. Some threads (whole warps) per token: the
+// token's own row is read (or written) once, its top_k grouped rows are touched
+// with several loads of a thread in flight (choices times vectors of the row).
+// A CTA takes as many tokens as fit. Rows of the grouped matrix behind the last
+// group's are zero in permute's and the gradient's outputs; they are spread
+// over the CTAs.
 constexpr int kMoveThreads = 256;
-constexpr int kMoveJ = 8;  // choices of a token handled at once
 
 struct MoveParams {
     const void *src;           // permute: x; combine and gradient: y
@@ -240,16 +240,32 @@ struct MoveParams {
     float *dweights;
     int64_t tokens, n_rows;    // n_rows: rows of the grouped matrix
     int32_t k, top_k, groups;
+    int32_t lanes;             // threads of a token
     unsigned *status;
 };
 
-__device__ __forceinline__ int32_t checked_slot(const MoveParams &p, int64_t token, int j) {
-    const int32_t s = p.slots[token * p.top_k + j];
-    if (s >= p.n_rows) {
-        record_status(p.status, kSiteBadSlot);
-        return -1;
+// Slots of a token's choices j0 .. j0 + J - 1 and their weights (-1 and 0: none),
+// all loads in flight at once. A slot past the grouped matrix counts as none;
+// returns whether there was one (reported once the row's loads are under way:
+// an atomic in between would hold them back).
+template <int J>
+__device__ __forceinline__ bool choices_of(const MoveParams &p, int64_t token, int j0, bool live, int32_t (&slot)[J],
+                                           float (&w)[J]) {
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const bool in = live && j0 + j < p.top_k;
+        slot[j] = in ? __ldg(p.slots + token * p.top_k + j0 + j) : -1;
+        w[j] = in ? (p.weights ? __ldg(p.weights + token * p.top_k + j0 + j) : 1.0f) : 0.0f;
     }
-    return s;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const bool past = slot[j] >= (int32_t)p.n_rows;
+        bad |= past;
+        if (past) slot[j] = -1;
+        if (slot[j] < 0) w[j] = 0.0f;
+    }
+    return bad;
 }
 
 template <typename T, int VW>
@@ -261,106 +277,166 @@ __device__ __forceinline__ void zero_tail(const MoveParams &p) {
             V::store(static_cast<T *>(p.dst) + r * p.k + (int64_t)c * VW, V::zero());
 }
 
-template <typename T, int VW>
+// The row's vectors are walked U at a time; choices J at a time.
+template <typename T, int VW, int U>
 __global__ void __launch_bounds__(kMoveThreads) permute_kernel(const MoveParams p) {
     using V = Vec<T, VW>;
+    constexpr int J = 8;
     griddep_wait();
     griddep_launch();
-    const int64_t token = blockIdx.x;
+    const int64_t token = (int64_t)blockIdx.x * (blockDim.x / p.lanes) + threadIdx.x / p.lanes;
+    const int sub = threadIdx.x % p.lanes, nvec = p.k / VW;
     if (token < p.tokens) {
         const T *x = static_cast<const T *>(p.src) + token * p.k;
-        for (int j0 = 0; j0 < p.top_k; j0 += kMoveJ) {
-            int32_t slot[kMoveJ];
+        for (int j0 = 0; j0 < p.top_k; j0 += J) {
+            int32_t slot[J];
+            float w[J];
+            const bool bad = choices_of<J>(p, token, j0, true, slot, w);
+            for (int c0 = sub; c0 < nvec; c0 += U * p.lanes) {
+                typename V::P v[U];
 #pragma unroll
-            for (int j = 0; j < kMoveJ; ++j) slot[j] = j0 + j < p.top_k ? checked_slot(p, token, j0 + j) : -1;
-            for (int c = threadIdx.x; c < p.k / VW; c += blockDim.x) {
-                const typename V::P v = V::load(x + (int64_t)c * VW);
+                for (int u = 0; u < U; ++u) {
+                    const int c = c0 + u * p.lanes;
+                    v[u] = c < nvec ? V::load(x + (int64_t)c * VW) : V::zero();
+                }
 #pragma unroll
-                for (int j = 0; j < kMoveJ; ++j)
-                    if (slot[j] >= 0) V::store(static_cast<T *>(p.dst) + (int64_t)slot[j] * p.k + (int64_t)c * VW, v);
+                for (int j = 0; j < J; ++j) {
+                    if (slot[j] < 0) continue;
+                    T *dst = static_cast<T *>(p.dst) + (int64_t)slot[j] * p.k;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int c = c0 + u * p.lanes;
+                        if (c < nvec) V::store(dst + (int64_t)c * VW, v[u]);
+                    }
+                }
             }
+            if (bad) record_status(p.status, kSiteBadSlot);
         }
     }
     zero_tail<T, VW>(p);
 }
 
+// A vector as packed pairs of binary32 (VW even), or its value in the first of
+// a pair; acc += w v on them.
 template <typename T, int VW>
-__global__ void __launch_bounds__(kMoveThreads) combine_kernel(const MoveParams p) {
-    using V = Vec<T, VW>;
-    griddep_wait();
-    griddep_launch();
-    const int64_t token = blockIdx.x;
-    const T *y = static_cast<const T *>(p.src), *res = static_cast<const T *>(p.other);
-    T *out = static_cast<T *>(p.dst) + token * p.k;
-    for (int c = threadIdx.x; c < p.k / VW; c += blockDim.x) {
-        float acc[VW];
-        if (res) {
-            V::unpack(V::load(res + token * p.k + (int64_t)c * VW), acc);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VW; ++e) acc[e] = 0.0f;
-        }
-        for (int j0 = 0; j0 < p.top_k; j0 += kMoveJ) {
-            typename V::P v[kMoveJ];
-            float w[kMoveJ];
-#pragma unroll
-            for (int j = 0; j < kMoveJ; ++j) {
-                const int32_t s = j0 + j < p.top_k ? checked_slot(p, token, j0 + j) : -1;
-                v[j] = s >= 0 ? V::load(y + (int64_t)s * p.k + (int64_t)c * VW) : V::zero();
-                w[j] = s >= 0 ? (p.weights ? p.weights[token * p.top_k + j0 + j] : 1.0f) : 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < kMoveJ; ++j) {
-                float f[VW];
-                V::unpack(v[j], f);
-#pragma unroll
-                for (int e = 0; e < VW; ++e) acc[e] = fmaf(w[j], f[e], acc[e]);
-            }
-        }
-        V::store(out + (int64_t)c * VW, V::pack(acc));
+__device__ __forceinline__ void widen_pairs(typename Vec<T, VW>::P v, uint64_t (&f)[(VW + 1) / 2]) {
+    if constexpr (VW > 1) {
+        Vec<T, VW>::unpack2(v, f);
+    } else {
+        float t[VW];
+        Vec<T, VW>::unpack(v, t);
+        f[0] = pk2(t[0], 0.0f);
     }
 }
-
-// Four choices at a time keep a thread within 64 registers, so that four CTAs
-// (32 warps) of an SM overlap their loads, sums and stores: 61 us with eight at
-// a time and two CTAs, 48 us like this (32768 rows of 2048, bf16).
-constexpr int kBackJ = 4;
-
 template <typename T, int VW>
-__global__ void __launch_bounds__(kMoveThreads, 4) combine_bwd_kernel(const MoveParams p) {
+__device__ __forceinline__ void add_scaled(uint64_t (&acc)[(VW + 1) / 2], float w, typename Vec<T, VW>::P v) {
+    uint64_t f[(VW + 1) / 2];
+    widen_pairs<T, VW>(v, f);
+    const uint64_t w2 = pk2(w, w);
+#pragma unroll
+    for (int e = 0; e < (VW + 1) / 2; ++e) acc[e] = fma2(w2, f[e], acc[e]);
+}
+
+// MORE: top_k > J, the choices in turns of J. Four CTAs per SM: left to itself the
+// compiler takes fewer registers and waits for its loads one by one (35.7 us
+// against 30.6 for 4096 x 8 rows of 2048 in fp16).
+template <typename T, int VW, int J, int U, bool MORE>
+__global__ void __launch_bounds__(kMoveThreads, 4) combine_kernel(const MoveParams p) {
     using V = Vec<T, VW>;
-    __shared__ float red[2][kBackJ][kMoveThreads / 32];
     griddep_wait();
     griddep_launch();
-    const int64_t token = blockIdx.x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    if (token < p.tokens) {
-        const T *y = static_cast<const T *>(p.src), *dout = static_cast<const T *>(p.other) + token * p.k;
-        T *dy = static_cast<T *>(p.dst);
-        for (int j0 = 0, parity = 0; j0 < p.top_k; j0 += kBackJ, parity ^= 1) {
-            int32_t slot[kBackJ];
-            float w[kBackJ], dot[kBackJ];
+    const int64_t token = (int64_t)blockIdx.x * (blockDim.x / p.lanes) + threadIdx.x / p.lanes;
+    const int sub = threadIdx.x % p.lanes, nvec = p.k / VW;
+    if (token >= p.tokens) return;
+    const T *y = static_cast<const T *>(p.src), *res = static_cast<const T *>(p.other);
+    T *out = static_cast<T *>(p.dst) + token * p.k;
+    bool bad = false;
+    for (int c0 = sub; c0 < nvec; c0 += U * p.lanes) {
+        uint64_t acc[U][(VW + 1) / 2];
 #pragma unroll
-            for (int j = 0; j < kBackJ; ++j) {
-                slot[j] = j0 + j < p.top_k ? checked_slot(p, token, j0 + j) : -1;
-                w[j] = slot[j] >= 0 ? p.weights[token * p.top_k + j0 + j] : 0.0f;
-                dot[j] = 0.0f;
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * p.lanes;
+            widen_pairs<T, VW>(res && c < nvec ? V::load(res + token * p.k + (int64_t)c * VW) : V::zero(), acc[u]);
+        }
+        int j0 = 0;
+        do {
+            typename V::P v[U][J];
+            int32_t slot[J];
+            float w[J];
+            bad |= choices_of<J>(p, token, j0, true, slot, w);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int c = c0 + u * p.lanes;
+                    v[u][j] = slot[j] >= 0 && c < nvec ? V::load(y + (int64_t)slot[j] * p.k + (int64_t)c * VW) : V::zero();
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < J; ++j) add_scaled<T, VW>(acc[u], w[j], v[u][j]);
+            j0 += J;
+        } while (MORE && j0 < p.top_k);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * p.lanes;
+            if (c >= nvec) continue;
+            if constexpr (VW > 1) {
+                V::store(out + (int64_t)c * VW, V::pack2(acc[u]));
+            } else {
+                const float f[VW] = {up2(acc[u][0]).x};
+                V::store(out + (int64_t)c * VW, V::pack(f));
             }
-            for (int c = threadIdx.x; c < p.k / VW; c += blockDim.x) {
-                const int64_t at = (int64_t)c * VW;
-                typename V::P v[kBackJ];
+        }
+    }
+    if (bad) record_status(p.status, kSiteBadSlot);
+}
+
+// At most four choices at a time keep a thread within 64 registers, so that
+// four CTAs (32 warps) of an SM overlap their loads, sums and stores: 61 us with
+// eight at a time and two CTAs, 48 us like this (32768 rows of 2048, bf16).
+template <typename T, int VW, int J, int U>
+__global__ void __launch_bounds__(kMoveThreads, 4) combine_bwd_kernel(const MoveParams p) {
+    using V = Vec<T, VW>;
+    __shared__ float red[2][J][kMoveThreads / 32];
+    griddep_wait();
+    griddep_launch();
+    const int64_t token = (int64_t)blockIdx.x * (blockDim.x / p.lanes) + threadIdx.x / p.lanes;
+    const int sub = threadIdx.x % p.lanes, nvec = p.k / VW;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warps = p.lanes >> 5, warp0 = (int)threadIdx.x / p.lanes * warps;  // of this token
+    const bool live = token < p.tokens;
+    const T *y = static_cast<const T *>(p.src), *dout = static_cast<const T *>(p.other) + (live ? token : 0) * p.k;
+    T *dy = static_cast<T *>(p.dst);
+    for (int j0 = 0, parity = 0; p.tokens > 0 && j0 < p.top_k; j0 += J, parity ^= 1) {
+        int32_t slot[J];
+        float w[J], dot[J];
+        const bool bad = choices_of<J>(p, token, j0, live, slot, w);
 #pragma unroll
-                for (int j = 0; j < kBackJ; ++j)
-                    v[j] = slot[j] >= 0 ? V::load(y + (int64_t)slot[j] * p.k + at) : V::zero();
-                const typename V::P dv = V::load(dout + at);
+        for (int j = 0; j < J; ++j) dot[j] = 0.0f;
+        for (int c0 = sub; c0 < nvec; c0 += U * p.lanes) {
+            typename V::P v[U][J], dv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * p.lanes;
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    v[u][j] = slot[j] >= 0 && c < nvec ? V::load(y + (int64_t)slot[j] * p.k + (int64_t)c * VW) : V::zero();
+                dv[u] = c < nvec ? V::load(dout + (int64_t)c * VW) : V::zero();
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * p.lanes;
+                if (c >= nvec) continue;
+                const int64_t at = (int64_t)c * VW;
                 if constexpr (VW > 1) {
                     uint64_t d[VW / 2];
-                    V::unpack2(dv, d);
+                    V::unpack2(dv[u], d);
 #pragma unroll
-                    for (int j = 0; j < kBackJ; ++j) {
+                    for (int j = 0; j < J; ++j) {
                         if (slot[j] < 0) continue;
                         uint64_t f[VW / 2], sum = 0;
-                        V::unpack2(v[j], f);
+                        V::unpack2(v[u][j], f);
 #pragma unroll
                         for (int e = 0; e < VW / 2; ++e) sum = fma2(d[e], f[e], sum);
                         const float2 t = up2(sum);
@@ -372,49 +448,74 @@ __global__ void __launch_bounds__(kMoveThreads, 4) combine_bwd_kernel(const Move
                     }
                 } else {
                     float d[VW];
-                    V::unpack(dv, d);
+                    V::unpack(dv[u], d);
 #pragma unroll
-                    for (int j = 0; j < kBackJ; ++j) {
+                    for (int j = 0; j < J; ++j) {
                         if (slot[j] < 0) continue;
                         float f[VW];
-                        V::unpack(v[j], f);
+                        V::unpack(v[u][j], f);
                         dot[j] = fmaf(d[0], f[0], dot[j]);
                         f[0] = w[j] * d[0];
                         V::store(dy + (int64_t)slot[j] * p.k + at, V::pack(f));
                     }
                 }
             }
-            // Sums of the four over the warp: lanes 8 q .. 8 q + 7 go on with
-            // the q-th.
-            const bool hi = lane & 16, odd = lane & 8;
-            float a = (hi ? dot[2] : dot[0]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? dot[0] : dot[2], 16);
-            float b = (hi ? dot[3] : dot[1]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? dot[1] : dot[3], 16);
-            float s = (odd ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 8);
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-            if ((lane & 7) == 0) red[parity][lane >> 3][warp] = s;
-            __syncthreads();
-            if (threadIdx.x < kBackJ && j0 + (int)threadIdx.x < p.top_k) {
-                float t = 0.0f;
-                for (int i = 0; i < warps; ++i) t += red[parity][threadIdx.x][i];
-                p.dweights[token * p.top_k + j0 + threadIdx.x] = t;
-            }
         }
+        // The warp's sums: lanes 32 / J * q and on go on with the q-th.
+        float s;
+        if constexpr (J == 4) {
+            const bool hi = lane & 16, odd = lane & 8;
+            const float a = (hi ? dot[2] : dot[0]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? dot[0] : dot[2], 16);
+            const float b = (hi ? dot[3] : dot[1]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? dot[1] : dot[3], 16);
+            s = (odd ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 8);
+        } else if constexpr (J == 2) {
+            const bool hi = lane & 16;
+            s = (hi ? dot[1] : dot[0]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? dot[0] : dot[1], 16);
+        } else {
+            s = dot[0];
+        }
+#pragma unroll
+        for (int o = 16 / J; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (lane % (32 / J) == 0) red[parity][lane / (32 / J)][warp] = s;
+        __syncthreads();
+        if (live && sub < J && j0 + sub < p.top_k) {
+            float t = 0.0f;
+            for (int i = 0; i < warps; ++i) t += red[parity][sub][warp0 + i];
+            p.dweights[token * p.top_k + j0 + sub] = t;
+        }
+        if (bad) record_status(p.status, kSiteBadSlot);
     }
     zero_tail<T, VW>(p);
 }
 
 enum class Move { kPermute, kCombine, kCombineBwd };
 
+// Threads of a token so that each has about U vectors of its row: whole warps,
+// a power of two of them, at most a CTA.
+static int move_lanes(int nvec, int u) {
+    int l = 32;
+    while (l < kMoveThreads && l * u < nvec) l *= 2;
+    return l;
+}
+
 template <typename T, int VW>
-static sharq_status move_run(LaunchCtx &ctx, Move what, const MoveParams &p) {
-    int threads = (int)round_up(p.k / VW, 32);
-    if (threads > kMoveThreads) threads = kMoveThreads;
-    const int64_t grid = p.tokens > 0 ? p.tokens : 1;
+static sharq_status move_run(LaunchCtx &ctx, Move what, MoveParams p) {
+    const int nvec = p.k / VW;
+    auto run = [&](auto kernel, int u) {
+        p.lanes = move_lanes(nvec, u);
+        const int64_t per = kMoveThreads / p.lanes, grid = p.tokens > 0 ? (p.tokens + per - 1) / per : 1;
+        return launch_pdl(ctx, kernel, grid, kMoveThreads, 0, 1, p);
+    };
     switch (what) {
-        case Move::kPermute: return launch_pdl(ctx, permute_kernel<T, VW>, grid, threads, 0, 1, p);
-        case Move::kCombine: return launch_pdl(ctx, combine_kernel<T, VW>, grid, threads, 0, 1, p);
-        default: return launch_pdl(ctx, combine_bwd_kernel<T, VW>, grid, threads, 0, 1, p);
+        case Move::kPermute: return p.top_k <= 2 ? run(permute_kernel<T, VW, 4>, 4) : run(permute_kernel<T, VW, 1>, 1);
+        case Move::kCombine:
+            return p.top_k == 1   ? run(combine_kernel<T, VW, 1, 2, false>, 2)
+                   : p.top_k == 2 ? run(combine_kernel<T, VW, 2, 2, false>, 2)
+                   : p.top_k <= 4 ? run(combine_kernel<T, VW, 4, 1, false>, 1)
+                   : p.top_k <= 8 ? run(combine_kernel<T, VW, 8, 1, false>, 1) : run(combine_kernel<T, VW, 8, 1, true>, 1);
+        default:
+            return p.top_k == 1   ? run(combine_bwd_kernel<T, VW, 1, 4>, 4)
+                   : p.top_k == 2 ? run(combine_bwd_kernel<T, VW, 2, 2>, 2) : run(combine_bwd_kernel<T, VW, 4, 1>, 1);
     }
 }
 
