@@ -31,7 +31,7 @@ namespace sq {
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteFew = 256;     // threads where entries and groups are few
 constexpr int kRouteCluster = 8;
-constexpr int kRouteKeep = 4;      // steps of 32 entries whose groups and places a lane keeps in registers
+constexpr int kRouteKeep = 8;      // steps of 32 entries whose groups and places a lane keeps in registers
 
 struct RouteParams {
     const void *ids;
