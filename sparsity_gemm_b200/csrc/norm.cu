@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
 // reduction of the partial rows.
 constexpr int kRingMax = 8;            // most rows in a ring
 constexpr int kRingBytes = 160 << 10;  // shared memory of an SM's rings
+constexpr int kRingEnough = 3;         // rows of a ring where an SM has several (more measured no faster)
 
 // FULL: every thread has all its columns.
 template <typename T, int VW, int MAXT, bool FULL>
@@ -799,8 +800,9 @@ static sharq_status norm_bwd(LaunchCtx &ctx, const NormBwdParams &p) {
     const int threads = bwd_threads(p.k);
     if constexpr (VW > 1) {
         const int64_t pair = 2 * 16 * (p.k / VW);
-        const int64_t fit = kRingBytes / bwd_per_sm(threads) / pair;
-        const int stages = fit > kRingMax ? kRingMax : (int)fit;  // at least 2: a pair of rows has at most 64 KB
+        const int per_sm = bwd_per_sm(threads), most = per_sm > 1 ? kRingEnough : kRingMax;
+        const int64_t fit = kRingBytes / per_sm / pair;  // at least 2: a pair of rows has at most 64 KB
+        const int stages = fit > most ? most : (int)fit;
         const bool full = p.k % ((int64_t)threads * kBwdCols) == 0;
         auto run = [&](auto kernel) {
             return launch_pdl(ctx, kernel, p.parts, threads, (size_t)(stages * pair), 1, p, stages, ctx.wait_ns, ctx.status);
