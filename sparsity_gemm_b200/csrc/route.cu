@@ -140,7 +140,6 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
                 all += v;
             }
         }
-        cluster_arrive_relaxed();  // this thread reads no other CTA's counts any more
     } else {
         __syncthreads();
         if (g < p.groups) all = mine[g];
@@ -171,6 +170,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
         base[g] = first + before;
     }
     __syncthreads();
+    if (ctas > 1) cluster_arrive_relaxed();  // this CTA has used what it read of the others' counts
 
     auto put = [&](int32_t v, int32_t e, int32_t slot) {
         if (e < e1) {
