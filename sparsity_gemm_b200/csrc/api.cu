@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -578,7 +579,23 @@ static bool overlap(const void *p, int64_t pb, const void *q, int64_t qb) {
     return a && b && pb > 0 && qb > 0 && a < b + (uintptr_t)qb && b < a + (uintptr_t)pb;
 }
 
-// The same for matrices of m rows with row strides, in bytes; column slices
+// A buffer a call reads or writes, in bytes. Whether an output shares a byte
+// with an input or with another output.
+struct Range {
+    const void *at;
+    int64_t bytes;
+};
+static bool clash(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+    for (const Range *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Range &i : ins)
+            if (overlap(o->at, o->bytes, i.at, i.bytes)) return true;
+        for (const Range *q = outs.begin(); q != o; ++q)
+            if (overlap(o->at, o->bytes, q->at, q->bytes)) return true;
+    }
+    return false;
+}
+
+// overlap for matrices of m rows with row strides, in bytes; column slices
 // of one buffer (equal strides) share nothing if their columns are disjoint.
 static bool overlap_rows(const void *p, int64_t pld, int64_t pw, const void *q, int64_t qld, int64_t qw, int64_t m) {
     if (m <= 0 || !overlap(p, (m - 1) * pld + pw, q, (m - 1) * qld + qw)) return false;
@@ -600,8 +617,8 @@ sharq_status sharq_layer_norm(const void *x_dev, int64_t m_tok, int64_t k, const
     if (!x_dev || !y_dev || !aligned(x_dev, e) || !aligned(y_dev, e) || (ln_w_dev && !aligned(ln_w_dev, e)) ||
         (ln_b_dev && !aligned(ln_b_dev, e)) || (mean_dev && !aligned(mean_dev, 4)) || (rstd_dev && !aligned(rstd_dev, 4)))
         return SHARQ_ERR_INVALID_ARG;
-    if (overlap(y_dev, bytes, x_dev, bytes) || overlap(y_dev, bytes, ln_w_dev, k * e) ||
-        overlap(y_dev, bytes, ln_b_dev, k * e))
+    if (clash({{y_dev, bytes}, {mean_dev, 4 * m_tok}, {rstd_dev, 4 * m_tok}},
+              {{x_dev, bytes}, {ln_w_dev, k * e}, {ln_b_dev, k * e}}))
         return SHARQ_ERR_INVALID_ARG;
     const bool vec16 = (k * e) % 16 == 0 && aligned(x_dev, 16) && aligned(y_dev, 16) &&
                        (!ln_w_dev || aligned(ln_w_dev, 16)) && (!ln_b_dev || aligned(ln_b_dev, 16));
@@ -633,16 +650,18 @@ sharq_status sharq_layer_norm_backward(const void *dy_dev, const void *x_dev, in
         if (!aligned(dy_dev, e) || !aligned(x_dev, e) || !aligned(dx_dev, e) || !aligned(rstd_dev, 4) ||
             (mean_dev && !aligned(mean_dev, 4)) || (ln_w_dev && !aligned(ln_w_dev, e)))
             return SHARQ_ERR_INVALID_ARG;
-        if ((dx_dev != dy_dev && overlap(dx_dev, bytes, dy_dev, bytes)) || overlap(dx_dev, bytes, x_dev, bytes) ||
-            overlap(dx_dev, bytes, ln_w_dev, k * e))
-            return SHARQ_ERR_INVALID_ARG;
     }
     if ((dw_dev && !aligned(dw_dev, 4)) || (db_dev && !aligned(db_dev, 4))) return SHARQ_ERR_INVALID_ARG;
-    if (overlap(dw_dev, 4 * k, db_dev, 4 * k)) return SHARQ_ERR_INVALID_ARG;
-    if (dw_dev || db_dev || !sq::norm_bwd_one_pass(k)) {
-        if (m_tok > 0 && (!ws_dev || !aligned(ws_dev, sq::kAlign) || ws_bytes < sharq_layer_norm_backward_bytes(m_tok, k)))
-            return SHARQ_ERR_INVALID_ARG;
+    size_t need = 0;
+    if (m_tok > 0 && (dw_dev || db_dev || !sq::norm_bwd_one_pass(k))) {
+        need = sharq_layer_norm_backward_bytes(m_tok, k);
+        if (!ws_dev || !aligned(ws_dev, sq::kAlign) || ws_bytes < need) return SHARQ_ERR_INVALID_ARG;
     }
+    if (clash({{dx_dev, bytes}, {dw_dev, 4 * k}, {db_dev, 4 * k}, {ws_dev, (int64_t)need}},
+              {{x_dev, bytes}, {dx_dev == dy_dev ? nullptr : dy_dev, bytes}, {ln_w_dev, k * e}, {mean_dev, 4 * m_tok},
+               {rstd_dev, 4 * m_tok}}) ||
+        clash({{dw_dev, 4 * k}, {db_dev, 4 * k}, {ws_dev, (int64_t)need}}, {{dy_dev, bytes}}))
+        return SHARQ_ERR_INVALID_ARG;
     const bool vec16 = (k * e) % 16 == 0 && aligned(dy_dev, 16) && aligned(x_dev, 16) && aligned(dx_dev, 16) &&
                        (!ln_w_dev || aligned(ln_w_dev, 16));
     sq::LaunchCtx ctx;
@@ -670,10 +689,7 @@ sharq_status sharq_route(const void *ids_dev, int id_bytes, int64_t m_tok, int64
         if (!ids_dev || !rows_dev || !slots_dev || !aligned(ids_dev, id_bytes) || !aligned(rows_dev, 4) ||
             !aligned(slots_dev, 4))
             return SHARQ_ERR_INVALID_ARG;
-        const int64_t ob = 4 * (n_groups + 1);
-        if (overlap(rows_dev, 4 * n, ids_dev, n * id_bytes) || overlap(slots_dev, 4 * n, ids_dev, n * id_bytes) ||
-            overlap(offsets_dev, ob, ids_dev, n * id_bytes) || overlap(rows_dev, 4 * n, slots_dev, 4 * n) ||
-            overlap(offsets_dev, ob, rows_dev, 4 * n) || overlap(offsets_dev, ob, slots_dev, 4 * n))
+        if (clash({{offsets_dev, 4 * (n_groups + 1)}, {rows_dev, 4 * n}, {slots_dev, 4 * n}}, {{ids_dev, n * id_bytes}}))
             return SHARQ_ERR_INVALID_ARG;
     }
     sq::LaunchCtx ctx;
@@ -691,7 +707,10 @@ sharq_status sharq_permute_rows(const void *x_dev, int64_t m_tok, int64_t k, con
     if (m_tok == 0) return SHARQ_OK;
     const int64_t e = dtype_bytes(dtype);
     if (!x_dev || !out_dev || !slots_dev || !offsets_dev || !aligned(x_dev, e) || !aligned(out_dev, e) ||
-        !aligned(slots_dev, 4) || !aligned(offsets_dev, 4) || overlap(x_dev, m_tok * k * e, out_dev, m_tok * top_k * k * e))
+        !aligned(slots_dev, 4) || !aligned(offsets_dev, 4))
+        return SHARQ_ERR_INVALID_ARG;
+    if (clash({{out_dev, m_tok * top_k * k * e}},
+              {{x_dev, m_tok * k * e}, {slots_dev, 4 * m_tok * top_k}, {offsets_dev, 4 * (n_groups + 1)}}))
         return SHARQ_ERR_INVALID_ARG;
     const bool vec16 = (k * e) % 16 == 0 && aligned(x_dev, 16) && aligned(out_dev, 16);
     sq::LaunchCtx ctx;
@@ -712,8 +731,8 @@ sharq_status sharq_combine(const void *y_dev, int64_t rows, int64_t m_tok, int64
     if ((rows > 0 && !y_dev) || !out_dev || !slots_dev || !aligned(y_dev, e) || !aligned(out_dev, e) ||
         !aligned(slots_dev, 4) || (weights_dev && !aligned(weights_dev, 4)) || (residual_dev && !aligned(residual_dev, e)))
         return SHARQ_ERR_INVALID_ARG;
-    if (overlap(out_dev, bytes, y_dev, rows * k * e) ||
-        (out_dev != residual_dev && overlap(out_dev, bytes, residual_dev, bytes)))
+    if (clash({{out_dev, bytes}}, {{y_dev, rows * k * e}, {out_dev == residual_dev ? nullptr : residual_dev, bytes},
+                                   {slots_dev, 4 * m_tok * top_k}, {weights_dev, 4 * m_tok * top_k}}))
         return SHARQ_ERR_INVALID_ARG;
     const bool vec16 = (k * e) % 16 == 0 && aligned(y_dev, 16) && aligned(out_dev, 16) &&
                        (!residual_dev || aligned(residual_dev, 16));
@@ -740,8 +759,9 @@ sharq_status sharq_combine_backward(const void *dout_dev, const void *y_dev, int
     if (!aligned(dout_dev, e) || !aligned(y_dev, e) || !aligned(dy_dev, e) || !aligned(slots_dev, 4) ||
         !aligned(weights_dev, 4) || !aligned(dweights_dev, 4))
         return SHARQ_ERR_INVALID_ARG;
-    if (overlap(dy_dev, gbytes, y_dev, gbytes) || overlap(dy_dev, gbytes, dout_dev, bytes) ||
-        overlap(dweights_dev, 4 * m_tok * top_k, weights_dev, 4 * m_tok * top_k))
+    if (clash({{dy_dev, gbytes}, {dweights_dev, 4 * m_tok * top_k}},
+              {{y_dev, gbytes}, {dout_dev, bytes}, {slots_dev, 4 * m_tok * top_k}, {weights_dev, 4 * m_tok * top_k},
+               {offsets_dev, 4 * (n_groups + 1)}}))
         return SHARQ_ERR_INVALID_ARG;
     const bool vec16 = (k * e) % 16 == 0 && aligned(dout_dev, 16) && aligned(y_dev, 16) && aligned(dy_dev, 16);
     sq::LaunchCtx ctx;
@@ -785,7 +805,11 @@ sharq_status sharq_lora(const void *x_dev, int64_t ldx, int64_t m_tok, int64_t k
     if (overlap_rows(out_dev, 2 * ldo, 2 * n_out, x_dev, 2 * ldx, 2 * k, m_tok) ||
         (base_dev && base_dev != out_dev &&
          overlap_rows(out_dev, 2 * ldo, 2 * n_out, base_dev, 2 * ldbase, 2 * n_out, m_tok)) ||
-        overlap(out_dev, span, a_dev, n_groups * rank * k * 2) || overlap(out_dev, span, b_dev, n_groups * rank * n_out * 2))
+        clash({{out_dev, span}, {ws_dev, (int64_t)need}},
+              {{a_dev, n_groups * rank * k * 2}, {b_dev, n_groups * rank * n_out * 2}, {scales_dev, 4 * n_groups},
+               {offsets_dev, 4 * (n_groups + 1)}, {rows_dev, 4 * m_tok}, {slots_dev, 4 * m_tok}}) ||
+        overlap(ws_dev, (int64_t)need, x_dev, ((m_tok - 1) * ldx + k) * 2) ||
+        overlap(ws_dev, (int64_t)need, base_dev, ((m_tok - 1) * ldbase + n_out) * 2))
         return SHARQ_ERR_INVALID_ARG;
     sq::LaunchCtx ctx;
     sharq_status st = make_ctx(stream, ctx);

@@ -118,6 +118,36 @@ def test_lora_refusals(L):
     assert call(x=P(1), ldx=512, out=P(1, 2 * 400), ldo=512) == sq.ERR_INVALID_ARG  # wraps into the next row's x
 
 
+def test_outputs_share_nothing(L):
+    """Outputs, workspaces among them, that reach into any other buffer."""
+    norm = lambda y=P(4), mean=P(5), rstd=P(6): L.sharq_layer_norm(  # noqa: E731
+        P(1), 8, 256, P(2), P(3), 1e-5, 0, 0, y, mean, rstd, None)
+    for bad in (dict(mean=P(1, 4092)), dict(rstd=P(2)), dict(rstd=P(5, 28)), dict(mean=P(4, 16)), dict(y=P(6, 16))):
+        assert norm(**bad) == sq.ERR_INVALID_ARG, bad
+    need = L.sharq_layer_norm_backward_bytes(8, 256)
+    back = lambda dx=P(6), dw=P(7), db=P(8), ws=P(9): L.sharq_layer_norm_backward(  # noqa: E731
+        P(1), P(2), 8, 256, P(3), P(4), P(5), 0, 0, dx, dw, db, ws, need, None)
+    for bad in (dict(dx=P(4)), dict(dx=P(5, 16)), dict(dw=P(1)), dict(dw=P(1), dx=P(1)), dict(db=P(2, 4)), dict(dw=P(3)),
+                dict(db=P(5)), dict(dw=P(6, 4092)), dict(ws=P(1)), dict(ws=P(2, 256)), dict(ws=P(3)), dict(ws=P(6)),
+                dict(ws=P(7)), dict(db=P(9, 2044))):
+        assert back(**bad) == sq.ERR_INVALID_ARG, bad
+    for bad in (P(2), P(2, 64), P(3)):
+        assert L.sharq_permute_rows(P(1), 10, 64, P(2), 2, P(3), 4, 0, bad, None) == sq.ERR_INVALID_ARG
+    for bad in (P(2, 64), P(3)):
+        assert L.sharq_combine(P(1), 20, 10, 64, P(2), P(3), 2, P(4), 0, bad, None) == sq.ERR_INVALID_ARG
+    grad = lambda dy=P(6), dw=P(7): L.sharq_combine_backward(  # noqa: E731
+        P(1), P(2), 20, 10, 64, P(3), P(4), 2, P(5), 4, 0, dy, dw, None)
+    for bad in (dict(dy=P(3)), dict(dy=P(4)), dict(dy=P(5)), dict(dw=P(1)), dict(dw=P(2, 128)), dict(dw=P(3, 76)),
+                dict(dw=P(5, 16)), dict(dw=P(6, 1024))):
+        assert grad(**bad) == sq.ERR_INVALID_ARG, bad
+    need = L.sharq_lora_bytes(4096, 16, 4)
+    lora = lambda out=P(9), ws=P(10): L.sharq_lora(  # noqa: E731
+        P(1), 512, 4096, 256, P(2), P(3), 128, 16, 4, P(4), P(5), P(6), P(7), 0, P(8), 256, out, 256, ws, need, None)
+    for bad in (dict(out=P(4)), dict(out=P(5)), dict(out=P(6, 16)), dict(out=P(7)), dict(out=P(10, 512)), dict(ws=P(1, 256)),
+                dict(ws=P(2)), dict(ws=P(3)), dict(ws=P(4)), dict(ws=P(5)), dict(ws=P(6)), dict(ws=P(7)), dict(ws=P(8))):
+        assert lora(**bad) == sq.ERR_INVALID_ARG, bad
+
+
 def _t(*shape, dtype=torch.float16):
     return _as_cuda(torch.zeros(shape, dtype=dtype))
 
