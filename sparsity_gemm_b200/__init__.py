@@ -598,10 +598,11 @@ def _take(t, name: str, dev: int, dtype, shape, rows: bool = False):
 
 def _no_grad(*ts):
     """The calls below are not recorded by autograd; a call that would lose a
-    gradient silently is refused (the *_backward calls are the gradients)."""
+    gradient silently, or write to a tensor that wants one, is refused (the
+    *_backward calls are the gradients)."""
     for t in ts:
         if t is not None and t.requires_grad:
-            raise ValueError("inputs that require a gradient are refused: call under torch.no_grad() and use the "
+            raise ValueError("tensors that require a gradient are refused: call under torch.no_grad() and use the "
                              "backward calls")
 
 
@@ -655,7 +656,7 @@ def layer_norm(x: torch.Tensor, w=None, b=None, eps: float = 1e-5, norm: str = "
         _require(kind == 0, "RMSNorm takes no b")
         _take(b, "b", dev, dt, (k,))
     if torch.is_grad_enabled():
-        _no_grad(x, w, b)
+        _no_grad(x, w, b, out)
     if out is None:
         out = _new_like(x, stream)
     else:
@@ -694,7 +695,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean, rstd: torch.Ten
     if w is not None:
         _take(w, "w", dev, dt, (k,))
     if torch.is_grad_enabled():
-        _no_grad(dy, x, w)
+        _no_grad(dy, x, w, out)
     if out is None:
         out = _new_like(x, stream)
     else:
@@ -728,7 +729,7 @@ class Routing:
     def __init__(self, offsets: torch.Tensor, rows: torch.Tensor, slots: torch.Tensor):
         self.dev = dev = _first(slots, "slots", 2, False, _i32)
         self.m_tok, self.top_k = slots.shape
-        self.groups = offsets.numel() - 1
+        self.groups = offsets.numel() - 1 if isinstance(offsets, torch.Tensor) else 0
         _take(offsets, "offsets", dev, _i32, (self.groups + 1,))
         _take(rows, "rows", dev, _i32, (self.m_tok * self.top_k,))
         _require(self.groups >= 1 and self.top_k >= 1, "a routing has at least one group and one entry per token")
@@ -770,8 +771,8 @@ def permute_rows(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = N
     _routing(routing, dev)
     m_tok, k = x.shape
     _require(routing.m_tok == m_tok, "routing is of another number of tokens")
-    if x.requires_grad and torch.is_grad_enabled():
-        _no_grad(x)
+    if torch.is_grad_enabled():
+        _no_grad(x, out)
     shape = (m_tok * routing.top_k, k)
     if out is None:
         out = _new(x, shape, x.dtype, stream)
@@ -799,7 +800,7 @@ def combine(y: torch.Tensor, routing: Routing, weights: torch.Tensor | None = No
     if residual is not None:
         _take(residual, "residual", dev, dt, (m_tok, k))
     if torch.is_grad_enabled():
-        _no_grad(y, weights, residual)
+        _no_grad(y, weights, residual, out)
     if out is None:
         out = _new(y, (m_tok, k), dt, stream)
     else:
@@ -871,7 +872,7 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, routing: Routing, sc
         _take(base, "base", dev, dt, (m_tok, n_out), True)
         ldbase = base.stride(0) if m_tok > 1 else n_out
     if torch.is_grad_enabled():
-        _no_grad(x, a, b, scales, base)
+        _no_grad(x, a, b, scales, base, out)
     if out is None:
         out = _new(x, (m_tok, n_out), dt, stream)
         ldo = n_out

@@ -241,6 +241,27 @@ def test_binding_refuses_to_lose_a_gradient(here):
     assert here.sharq_layer_norm.called
 
 
+def test_binding_refuses_outputs_that_require_a_gradient(here):
+    x, r, r1 = _t(6, 64), _routing(), _routing(6, 1)
+    stat = _t(6, dtype=torch.float32)
+
+    def leaf(*shape):
+        return _as_cuda(torch.zeros(shape, dtype=torch.float16, requires_grad=True))
+
+    for f in (lambda: sq.layer_norm(x, out=leaf(6, 64)), lambda: sq.layer_norm_backward(x, x, stat, stat, out=leaf(6, 64)),
+              lambda: sq.permute_rows(x, r, out=leaf(12, 64)), lambda: sq.combine(_t(12, 64), r, out=leaf(6, 64)),
+              lambda: sq.lora(x, _t(3, 16, 64), _t(3, 32, 16), r1, out=leaf(6, 32))):
+        with pytest.raises(ValueError, match="require a gradient"):
+            f()
+
+
+def test_routing_refuses_other_objects(here):
+    r = _routing()
+    for args in ((None, r.rows, r.slots), (r.offsets, None, r.slots), (r.offsets, r.rows, None), ([0, 1], r.rows, r.slots)):
+        with pytest.raises(ValueError):
+            sq.Routing(*args)
+
+
 def test_valid_calls_reach_the_library(here):
     f32 = torch.float32
     x, r, r1 = _t(6, 64), _routing(), _routing(6, 1)
