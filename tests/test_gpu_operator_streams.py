@@ -1,6 +1,7 @@
 """The operators around the FP4 linear on streams other than the current one,
 on two streams at once, from two host threads, and in two captured graphs that
-share a memory pool and replay in turn: always the bits of a plain call."""
+share a memory pool and replay in turn, and on inputs rewritten right before:
+always the bits of a plain call."""
 import threading
 
 import pytest
@@ -121,6 +122,41 @@ def test_two_graphs_of_one_pool():
             torch.cuda.synchronize()
             got = [t.clone() for t in outs[i]]  # the other graph may use the same memory
             _same(got, _all(new))
+    assert sq.get_last_error() == sq.OK
+
+
+@pytest.mark.parametrize("m,rank,groups", [(96, 64, 3), (1100, 16, 5), (40, 16, 3)])
+def test_inputs_changed_right_before_a_call(m, rank, groups):
+    """Weights, adapters' ids, base and statistics that a small kernel rewrites
+    in place right before each call (the next one's first loads may already be
+    on their way): the results are those of tensors that were never touched."""
+    k, n, top_k, steps = 192, 328, 2, 48
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda").half()  # noqa: E731
+    x, a = r(m, k), r(groups, rank, k)
+    bs, bases, ws = r(steps, groups, n, rank), r(steps, m, n), r(steps, k)
+    ids = torch.randint(-1, groups, (steps, m), generator=gen, device="cuda", dtype=torch.int32)
+    eids = torch.randint(-1, groups, (steps, m, top_k), generator=gen, device="cuda", dtype=torch.int32)
+    ew = torch.rand(steps, m, top_k, generator=gen, device="cuda")
+
+    def step(b, base, w, i, e, v):
+        y, mean, rstd = sq.layer_norm(x, w, stats=True)
+        dx, dw, db = sq.layer_norm_backward(y, x, mean, rstd, w)
+        out = sq.lora(x, a, b, sq.route(i, groups), base=base)
+        q = sq.route(e, groups)
+        g = sq.permute_rows(y, q)
+        back = sq.combine(g, q, v, x)
+        return [y, dx, dw, db, out, g, back, *sq.combine_backward(y, g, q, v)]
+
+    mine = [t[0].clone() for t in (bs, bases, ws, ids, eids, ew)]
+    got = []
+    for s in range(steps):
+        for t, from_ in zip(mine, (bs, bases, ws, ids, eids, ew)):
+            t.copy_(from_[s])
+        got.append(step(*mine))
+    torch.cuda.synchronize()
+    for s in range(steps):
+        _same(got[s], step(bs[s], bases[s], ws[s], ids[s], eids[s], ew[s]))
     assert sq.get_last_error() == sq.OK
 
 
