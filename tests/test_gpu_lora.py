@@ -127,6 +127,44 @@ def test_column_slices():
     _check(c, buf[:, 96:])
 
 
+@pytest.mark.parametrize("m,rank", [(40000, 16), (40000, 64)])
+def test_row_offsets_pass_32_bits(m, rank):
+    """Columns of buffers whose element offsets pass 2^31 (65536 a row): the
+    last rows are those of compact copies, bit for bit."""
+    c = _case(m + rank, m, 64, 96, rank, 4, torch.float16)
+    xs = torch.empty(m, 65536, dtype=torch.float16, device="cuda")
+    ys = torch.empty(m, 65536, dtype=torch.float16, device="cuda")
+    x, y = xs[:, 65536 - 64:], ys[:, 65536 - 96:]
+    x.copy_(c["x"])
+    y.copy_(c["base"])
+    r = sq.route(c["ids"], 4)
+    sq.lora(x, c["a"], c["b"], r, scales=c["scales"], base=y, out=y)
+    assert torch.equal(y, _run(c))
+    _check(c, y.contiguous())
+    del x, y, xs, ys
+
+
+@pytest.mark.parametrize("m", [24, 17000])
+def test_adapter_offsets_pass_32_bits(m):
+    """A thousand adapters of 2^21 elements: the last ones' offsets pass 2^31.
+    A's rows are unit vectors, so h picks columns of x and is exact."""
+    groups, rank, k, n = 1024, 128, 16400, 32
+    a = torch.zeros(groups, rank, k, dtype=torch.float16, device="cuda")
+    cols = torch.arange(rank, device="cuda") * 128
+    a[:, torch.arange(rank, device="cuda"), cols] = 1.0
+    b = torch.zeros(groups, n, rank, dtype=torch.float16, device="cuda")
+    b[:, torch.arange(n, device="cuda"), torch.arange(n, device="cuda") * 3] = 1.0
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    x = torch.randint(-64, 64, (m, k), generator=gen, device="cuda").half()
+    ids = torch.randint(groups - 9, groups, (m,), generator=gen, device="cuda", dtype=torch.int32)
+    r = sq.route(ids, groups)
+    scales = torch.ones(groups, device="cuda") * 2.0
+    out = sq.lora(x, a, b, r, scales=scales)
+    assert torch.equal(out, 2 * x[:, cols[torch.arange(n, device="cuda") * 3]])
+    assert sq.get_last_error() == sq.OK
+    del a, b, x
+
+
 def test_nobody_or_everybody_has_an_adapter():
     for none in (0.0, 1.0):
         c = _case(4, 90, 256, 256, 16, 5, torch.float16, none=none)

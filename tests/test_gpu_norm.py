@@ -217,6 +217,24 @@ def test_long_row_offsets_pass_32_bits():
     del y, x
 
 
+@pytest.mark.parametrize("rows,k", [(33000, 65536), (270000, 8192), (270000, 8193)])
+def test_gradient_row_offsets_pass_32_bits(rows, k):
+    """The gradient where offsets pass 2^31: the last rows are those of a call
+    on these rows alone, bit for bit (a row's sums do not depend on its place)."""
+    x = torch.zeros(rows, k, dtype=torch.float16, device="cuda")
+    dy = torch.zeros(rows, k, dtype=torch.float16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    x[-8:] = torch.randn(8, k, generator=gen, device="cuda").half()
+    dy[-8:] = torch.randn(8, k, generator=gen, device="cuda").half()
+    _, mean, rstd = sq.layer_norm(x[-8:], stats=True)
+    means, rstds = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    means[-8:], rstds[-8:] = mean, rstd
+    dx, _, _ = sq.layer_norm_backward(dy, x, means, rstds, out=dy.clone())
+    want, _, _ = sq.layer_norm_backward(dy[-8:], x[-8:], mean, rstd)
+    assert torch.equal(dx[-8:], want) and not bool(dx[:8].any())
+    del dx, dy, x
+
+
 def test_other_streams_and_graph_replay():
     x, w, b, dy = _inputs(11, 64, 1536, torch.float16)
     want = sq.layer_norm(x, w, b, stats=True)

@@ -155,6 +155,30 @@ def test_rows_there_and_back_other_layouts():
     check_moves(50, 4, 8, 512, torch.float32, none=0.0, extra=13)  # grouped rows behind the last group
 
 
+@pytest.mark.parametrize("top_k,k", [(1, 65536), (2, 32768), (1, 32771)])
+def test_row_offsets_pass_32_bits(top_k, k):
+    """Grouped rows and tokens whose element offsets pass 2^31: copies and sums
+    with powers of two as weights are exact, so every bit is known."""
+    tokens = 33000 if k == 65536 else 66000 // top_k if k == 32768 else 65600
+    ids = torch.arange(tokens * top_k, device="cuda", dtype=torch.int32).view(tokens, top_k) % 2
+    r = sq.route(ids, 2)
+    pick = torch.tensor([0, 1, tokens // 2, tokens - 2, tokens - 1], device="cuda")
+    x = torch.zeros(tokens, k, dtype=torch.float16, device="cuda")
+    x[pick] = _values(1, (5, k), torch.float16)
+    moved = sq.permute_rows(x, r)
+    slots = r.slots.long()[pick]
+    for j in range(top_k):
+        assert torch.equal(moved[slots[:, j]], x[pick])
+    w = torch.full((tokens, top_k), 1.0 / top_k, device="cuda")
+    assert torch.equal(sq.combine(moved, r, w)[pick], x[pick])
+    dy, dw = sq.combine_backward(x, moved, r, w)
+    for j in range(top_k):
+        assert torch.equal(dy[slots[:, j]], (x[pick].float() / top_k).half())
+    sq2 = (x[pick].double() ** 2).sum(1, keepdim=True).expand(5, top_k)
+    _close("dweights", dw[pick], sq2, (k / 256 + 16) * U * sq2)
+    assert sq.get_last_error() == sq.OK
+
+
 def test_values_nobody_asked_for_do_not_leak():
     """NaN and infinity in grouped rows without an entry stay there."""
     ids = random_ids(6, 40, 2, 4, 0.4)
