@@ -168,6 +168,12 @@ __device__ __forceinline__ void cta_find_tile(const LoraParams &p, int32_t *off,
 // runs after the first of these loads and before h is read.
 constexpr int kAhead = 2;
 
+// Row stride of the two terms of h: a lane of a quarter-warp reads 16 bytes of
+// one of two rows, 64 bytes of each (rank up to 16: a half-warp 8 bytes of one of
+// four rows), and these fill the 32 banks.
+template <int NB>
+constexpr int kHLd = NB == 2 ? 16 : NB == 4 ? 32 : 8 * NB + 32;
+
 template <int MT>
 constexpr int kAheadBytes = kAhead * 2 * MT * 16 * kLoraThreads;
 
@@ -175,7 +181,7 @@ template <typename T, int MT, int NB, typename F>
 __device__ __forceinline__ void expand_tile(const LoraParams &p, int group, const int32_t *row_s, const float *scale_s,
                                             const uint16_t *hh, const uint16_t *hl, uint8_t *ahead, int c0, int c1,
                                             F ready) {
-    constexpr int kLd = 8 * NB + 8, kS = (NB + 3) / 4;
+    constexpr int kLd = kHLd<NB>, kS = (NB + 3) / 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
     const T *b = static_cast<const T *>(p.b) + (int64_t)group * p.n * p.rank;
     const T *base = static_cast<const T *>(p.base);
@@ -333,8 +339,8 @@ constexpr int kLoraCluster = 8;  // most CTAs of a tile
 template <int NB>
 struct LoraCfg {
     static constexpr int kRows = 16, kRank = 8 * NB;
-    static constexpr int kLd = kRank + 8;   // row stride of the binary32 parts and of the 16-bit terms
-    static constexpr int kSmem = kLoraWarps * kRows * kLd * 4 + 2 * kRows * kLd * 2 + kAheadBytes<1>;
+    static constexpr int kLd = kRank + 8;   // row stride of the binary32 parts
+    static constexpr int kSmem = kLoraWarps * kRows * kLd * 4 + 2 * kRows * kHLd<NB> * 2 + kAheadBytes<1>;
     static constexpr int kStep = NB >= 8 ? 1 : 2;  // steps of 32 elements of k in flight
 };
 
@@ -343,8 +349,8 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraParams p) 
     using C = LoraCfg<NB>;
     extern __shared__ __align__(16) uint8_t smem[];
     float *part = reinterpret_cast<float *>(smem);  // [warps][rows][kLd]; [0]: the CTA's sum
-    uint16_t *hh = reinterpret_cast<uint16_t *>(smem + kLoraWarps * C::kRows * C::kLd * 4);  // [rows][kLd]
-    uint16_t *hl = hh + C::kRows * C::kLd;
+    uint16_t *hh = reinterpret_cast<uint16_t *>(smem + kLoraWarps * C::kRows * C::kLd * 4);  // [rows][kHLd]
+    uint16_t *hl = hh + C::kRows * kHLd<NB>;
     __shared__ int32_t off[kGroupsMax + 1];
     __shared__ int32_t tile_s[3];
     __shared__ int32_t row_s[C::kRows];
@@ -470,8 +476,8 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraParams p) 
                         const float v = h[i] * down;
                         const T hi = narrow<T>(v);
                         const T lo = narrow<T>(v - widen(hi));
-                        memcpy(hh + r * C::kLd + c, &hi, 2);
-                        memcpy(hl + r * C::kLd + c, &lo, 2);
+                        memcpy(hh + r * kHLd<NB> + c, &hi, 2);
+                        memcpy(hl + r * kHLd<NB> + c, &lo, 2);
                     }
                 }
                 if (lane == 0) scale_s[r] = scale * up;
@@ -735,7 +741,7 @@ constexpr int kExPerSm = NB <= 4 ? 3 : 2;
 // the CTAs, which stay for the whole launch: a CTA's share ends inside a tile.
 template <typename T, int NB>
 __global__ void __launch_bounds__(kLoraThreads, kExPerSm<NB>) lora_expand_kernel(const LoraParams p) {
-    constexpr int R = 8 * NB, kLd = R + 8;
+    constexpr int R = 8 * NB, kLd = kHLd<NB>;
     extern __shared__ __align__(16) uint8_t ahead[];
     __shared__ __align__(16) uint16_t hh[kExRows * kLd], hl[kExRows * kLd];
     __shared__ int32_t off[kGroupsMax + 1], tiles[kGroupsMax + 1];
