@@ -47,8 +47,8 @@ struct LoraParams {
     int32_t bare_ctas;  // CTAs, the grid's first, that copy rows without a group
     unsigned *status;
     uint64_t wait_ns;
-    void *h;         // two-launch form: [grouped row][2][padded rank] 16-bit terms
-    float *hscale;   // and their power of two
+    float *part;          // two-launch form: the parts of h, [part][128 rows][padded rank]
+    int32_t shrink_ctas;  // and the CTAs that make them
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -80,6 +80,12 @@ __device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) { return __uint_as_float(ld_cluster_u32(addr)); }
+
+// The power of two that brings a row's largest value to [1, 2).
+__device__ __forceinline__ int row_exponent(float top) {
+    const int e = (int)(__float_as_uint(top) >> 23) - 127;
+    return e < -100 ? -100 : e > 126 ? 0 : e;
+}
 
 // The tile's group and rows, found by warp 0 in the offsets. tile_s: [0] group
 // (-1: no such tile, -2: bad offsets), [1] first grouped row, [2] rows.
@@ -465,9 +471,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraParams p) 
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                // a power of two that brings the row's largest value to [1, 2)
-                int e = (int)(__float_as_uint(top) >> 23) - 127;
-                e = e < -100 ? -100 : e > 126 ? 0 : e;
+                const int e = row_exponent(top);
                 const float down = pow2f(-e), up = pow2f(e);
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
@@ -496,48 +500,63 @@ __global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraParams p) 
 }
 
 // ---------------------------------------------------------------------------
-// Many rows per adapter: two launches, h in the workspace.
+// Many rows per adapter: two launches, parts of h in the workspace.
 //
 // The first computes h = x A^T on the tensor cores of the fifth generation:
 // 128 rows of a group per tile, gathered from x in 16-byte copies (a TMA gather
 // of four rows per copy measured 34 us against 24 for 8192 x 4096, rank 16),
 // A's rows beside them, k in steps of 64 through a ring of shared-memory
-// stages, the accumulator in tensor memory. The CTAs of a cluster split k and add their
-// parts through distributed shared memory; h leaves as its two 16-bit terms.
-// It is bound by reading x. The second is the one-launch form's second half on
-// tiles of 32 rows, bound by base and out. Two launches keep both streaming all
-// the time; in one, a tile's reads of x and its writes alternate.
+// stages, the accumulator in tensor memory. The tiles' steps, laid end to end,
+// are divided evenly among the CTAs; what a CTA has of a tile is a part of h,
+// which it leaves in the workspace while the next tile's copies are under way.
+// It is bound by reading x and A. The second adds the parts in order and is the
+// one-launch form's second half on tiles of 32 rows, bound by base and out. Two
+// launches keep both streaming all the time; in one, a tile's reads of x and its
+// writes alternate.
 constexpr int kShRows = 128;
 constexpr int kShK = 64;
-constexpr int kShThreads = 192;  // warps 0-3: copies of x, then the accumulator; 4: copies of A; 5: products
-constexpr int kShCopiers = 128;
+constexpr int kShThreads = 320;  // warps 0-3: copies of x; 4: copies of A; 5: products; 6-9: parts out
+constexpr int kShCopiers = 128, kShWriters = 128;
 constexpr int kShX = kShRows * kShK * 2;
+constexpr int kShParts = 8;      // CTAs per tile where there are more CTAs than that
 
 template <int R>
 struct ShrinkCfg {
     static constexpr int kStage = kShX + R * kShK * 2;
-    static constexpr int kStages = (R <= 64 ? 72 : 100) * 1024 / kStage;  // three CTAs on an SM (rank 128: two)
-    static constexpr int kLd = R + 4;                    // row stride of the binary32 parts
-    static constexpr int kPart = kShRows * kLd * 4;
-    static constexpr int kSmem = 1024 + (kStages * kStage > kPart ? kStages * kStage : kPart);
-    static constexpr int kTmem = R < 32 ? 32 : R;
+    static constexpr int kPerSm = R <= 64 ? 3 : 2;
+    static constexpr int kStages = (R <= 64 ? 72 : 100) * 1024 / kStage;
+    static constexpr int kSmem = 1024 + kStages * kStage;  // and the tables: two words per group, and one
+    static constexpr int kTmem = 2 * R;  // two accumulators
 };
 
 // Padded rank of the two-launch form.
 SQ_HD int shrink_rank(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
+// The division of the first launch: `total` tiles of `blocks` steps each among
+// up to `ctas` CTAs, each with at least one step. CTA i has the steps work * i /
+// ctas and on; its part of tile t is part number i + t of the workspace, so a
+// tile's parts lie one after another.
+struct Shares {
+    int64_t work;
+    int blocks, ctas;
+    __device__ __forceinline__ Shares(int total, int blocks_, int most)
+        : work((int64_t)total * blocks_), blocks(blocks_), ctas(min(most, total * min(blocks_, kShParts))) {}
+    __device__ __forceinline__ int64_t start(int i) const { return work * i / ctas; }
+    __device__ __forceinline__ int owner(int64_t step) const { return (int)(((step + 1) * ctas - 1) / work); }
+};
+
 template <typename T, int R>
-__global__ void __launch_bounds__(kShThreads, 2)
+__global__ void __launch_bounds__(kShThreads, ShrinkCfg<R>::kPerSm)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap tm_a, const LoraParams p) {
     using C = ShrinkCfg<R>;
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], done;
+    __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], made[2], taken[2];
     __shared__ uint32_t tmem_s;
-    __shared__ int32_t off[kGroupsMax + 1], tiles[kGroupsMax + 1];
     __shared__ int table_ok;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
-    float *part = reinterpret_cast<float *>(dyn + (ring - smem_u32(dyn)));
+    int32_t *off = reinterpret_cast<int32_t *>(dyn + (ring - smem_u32(dyn)) + C::kStages * C::kStage);  // [groups + 1]
+    int32_t *tiles = off + p.groups + 1;                                                               // [groups + 1]
     if (warp == 5) {
         tmem_alloc(smem_u32(&tmem_s), C::kTmem);
         tmem_relinquish();
@@ -547,15 +566,15 @@ __global__ void __launch_bounds__(kShThreads, 2)
             mbar_init(smem_u32(&full[s]), kShCopiers + 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
-        mbar_init(smem_u32(&done), 1);
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&made[a]), 1);
+            mbar_init(smem_u32(&taken[a]), kShWriters);
+        }
         mbar_fence_init();
     }
     tc_fence_before();
     griddep_wait();
     griddep_launch();
-    uint32_t csize;
-    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
-    const uint32_t crank = cluster_ctarank();
     for (int i = threadIdx.x; i <= p.groups; i += kShThreads) off[i] = p.offsets[i];
     __syncthreads();  // also publishes the set-up above
     tc_fence_after();
@@ -565,39 +584,32 @@ __global__ void __launch_bounds__(kShThreads, 2)
     }
     __syncthreads();
     const uint32_t tmem = tmem_s;
-    if (!table_ok) {  // the same for every CTA
-        if (blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, kSiteBadOffsets);
-        if (warp == 5) tmem_dealloc(tmem, C::kTmem);
-        return;
-    }
-    // How many CTAs share a tile: as many of a cluster as the tiles there are
-    // leave to each (the launch knows only how many adapters there are, not how
-    // many of them the batch uses).
-    const int total = tiles[p.groups], ctas = (int)gridDim.x;
-    int split = (int)csize;
-    while (split > 1 && (int64_t)total * split > ctas) split /= 2;
-    const uint32_t sub_rank = crank % split, lead = crank - sub_rank;
-    const int units = ctas / split, unit = (int)blockIdx.x / split;
-    const int blocks = (p.k + kShK - 1) / kShK;
-    const int b0 = (int)((int64_t)blocks * sub_rank / split), b1 = (int)((int64_t)blocks * (sub_rank + 1) / split);
-    int used = 0;  // ring stages used by the tiles before
-    uint32_t done_phase = 0;
-    // every CTA of a cluster takes as many steps: they meet in its barriers
-    for (int step = 0; step * units < total; ++step, done_phase ^= 1) {
-        const int tile = step * units + unit;
-        if (tile >= total) {
-            cluster_sync();
-            cluster_sync();
-            continue;
+    const int total = table_ok ? tiles[p.groups] : 0;
+    if (!table_ok && blockIdx.x == 0 && threadIdx.x == 0) record_status(p.status, kSiteBadOffsets);
+    const Shares share(total, (p.k + kShK - 1) / kShK, (int)gridDim.x);
+    const int me = (int)blockIdx.x;
+    const int64_t w0 = me < share.ctas ? share.start(me) : 0, w1 = me < share.ctas ? share.start(me + 1) : 0;
+
+    // Every role walks the same parts: f(number of the part here, tile, its group, steps b0 .. b1-1)
+    auto parts = [&](auto f) {
+        int n = 0;
+        for (int64_t w = w0; w < w1; ++n) {
+            const int tile = (int)(w / share.blocks), b0 = (int)(w % share.blocks);
+            const int b1 = (int)min((int64_t)share.blocks, b0 + w1 - w);
+            if (!f(n, tile, group_of_tile(tiles, p.groups, tile), b0, b1)) return;
+            w += b1 - b0;
         }
-        const int group = group_of_tile(tiles, p.groups, tile);
-        const int first = off[group] + (tile - tiles[group]) * kShRows, count = min(kShRows, off[group + 1] - first);
-        if (warp < 4) {
-            // 16-byte copies into the products' layout (128-byte rows, piece c of
-            // row r at c ^ (r % 8)): 8 threads per row, every 16th row. Rows past
-            // the tile's end are not copied: what their lanes of the accumulator
-            // hold is not read.
-            const int r0 = threadIdx.x >> 3, piece = threadIdx.x & 7;
+    };
+    if (warp < 4) {
+        // 16-byte copies into the products' layout (128-byte rows, piece c of
+        // row r at c ^ (r % 8)): 8 threads per row, every 16th row. Rows past
+        // the tile's end are not copied: what their lanes of the accumulator
+        // hold is not read.
+        const int r0 = threadIdx.x >> 3, piece = threadIdx.x & 7;
+        const uint32_t at = (uint32_t)(r0 * 128 + ((piece ^ (r0 & 7)) * 16));  // rows 16 apart: the same r % 8
+        int i = 0;
+        parts([&](int, int tile, int group, int b0, int b1) {
+            const int first = off[group] + (tile - tiles[group]) * kShRows, count = min(kShRows, off[group + 1] - first);
             const T *src[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -608,124 +620,92 @@ __global__ void __launch_bounds__(kShThreads, 2)
                     src[j] = static_cast<const T *>(p.x) + (int64_t)(v >= 0 && v < p.m ? v : 0) * p.ldx + piece * 8;
                 }
             }
-            const uint32_t at = (uint32_t)(r0 * 128 + ((piece ^ (r0 & 7)) * 16));  // rows 16 apart: the same r % 8
-            for (int b = b0; b < b1; ++b) {
-                const int i = used + b - b0, s = i % C::kStages;
+            for (int b = b0; b < b1; ++b, ++i) {
+                const int s = i % C::kStages;
                 const bool ok = mbar_wait_own(smem_u32(&empty[s]), ((i / C::kStages) & 1) ^ 1, p.status, kSiteLoraEmpty, p.wait_ns);
-                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                if (!__all_sync(0xFFFFFFFFu, ok)) return false;
                 const uint32_t dst = ring + s * C::kStage + at, in = b * kShK + piece * 8 < p.k ? 16u : 0u;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (src[j]) cp_async16_zfill(dst + j * 16 * 128, in ? src[j] + b * kShK : src[j], in);
                 cp_async_arrive(smem_u32(&full[s]));
             }
-            cp_async_wait<0>();
-        } else if (warp == 4) {
-            if (lane == 0) {
-                for (int b = b0; b < b1; ++b) {
-                    const int i = used + b - b0, s = i % C::kStages;
+            return true;
+        });
+        cp_async_wait<0>();
+    } else if (warp == 4) {
+        if (lane == 0) {
+            int i = 0;
+            parts([&](int, int, int group, int b0, int b1) {
+                for (int b = b0; b < b1; ++b, ++i) {
+                    const int s = i % C::kStages;
                     if (!mbar_wait_own(smem_u32(&empty[s]), ((i / C::kStages) & 1) ^ 1, p.status, kSiteLoraEmpty, p.wait_ns)) {
                         // gave up: let the copies in flight land before the CTA's shared memory goes
                         for (int f = i < C::kStages ? 0 : i - C::kStages; f < i; ++f)
                             (void)mbar_wait_own(smem_u32(&full[f % C::kStages]), (f / C::kStages) & 1, nullptr, 0, 10000000ull);
-                        break;
+                        return false;
                     }
                     const uint32_t bar = smem_u32(&full[s]);
                     mbar_arrive_expect_tx(bar, R * kShK * 2);
                     tma_load_2d(ring + s * C::kStage + kShX, &tm_a, b * kShK, group * p.rank, bar);
                 }
-            }
-            __syncwarp();
-        } else if (warp == 5) {
-            if (lane == 0) {
-                // D binary32; A and B of type T, both K-major; N = R, M = 128
-                const uint32_t fmt = IsBf16<T>::v ? 1u : 0u;
-                const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(R >> 3) << 17) | ((kShRows >> 4) << 24);
-                for (int b = b0; b < b1; ++b) {
-                    const int i = used + b - b0, s = i % C::kStages;
-                    if (!mbar_wait_own(smem_u32(&full[s]), (i / C::kStages) & 1, p.status, kSiteLoraFull, p.wait_ns)) break;
+                return true;
+            });
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        if (lane == 0) {
+            // D binary32; A and B of type T, both K-major; N = R, M = 128
+            const uint32_t fmt = IsBf16<T>::v ? 1u : 0u;
+            const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(R >> 3) << 17) | ((kShRows >> 4) << 24);
+            int i = 0;
+            parts([&](int n, int, int, int b0, int b1) {
+                const uint32_t acc = tmem + (n & 1) * R;
+                if (!mbar_wait_own(smem_u32(&taken[n & 1]), ((n >> 1) & 1) ^ 1, p.status, kSiteLoraTaken, p.wait_ns)) return false;
+                tc_fence_after();
+                for (int b = b0; b < b1; ++b, ++i) {
+                    const int s = i % C::kStages;
+                    if (!mbar_wait_own(smem_u32(&full[s]), (i / C::kStages) & 1, p.status, kSiteLoraFull, p.wait_ns)) return false;
                     fence_proxy_async();  // x came through the generic proxy
                     tc_fence_after();
                     const uint32_t st = ring + s * C::kStage;
                     const uint64_t dx = smem_desc(st, 16, 8 * kShK * 2, 2u), da = smem_desc(st + kShX, 16, 8 * kShK * 2, 2u);
 #pragma unroll
-                    for (int j = 0; j < kShK / 16; ++j) tc_mma_f16(tmem, dx + 2 * j, da + 2 * j, idesc, b != b0 || j != 0);
+                    for (int j = 0; j < kShK / 16; ++j) tc_mma_f16(acc, dx + 2 * j, da + 2 * j, idesc, b != b0 || j != 0);
                     tc_commit(smem_u32(&empty[s]));
                 }
-                tc_commit(smem_u32(&done));
-            }
-            __syncwarp();
+                tc_commit(smem_u32(&made[n & 1]));
+                return true;
+            });
         }
-        // Every thread waits for the products: the ring is free then, and the
-        // parts of h take its place.
-        const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_own(smem_u32(&done), done_phase, p.status, kSiteLoraDone, p.wait_ns));
-        tc_fence_after();
-        if (warp < 4) {
-            float *row = part + (warp * 32 + lane) * C::kLd;
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3, row = quarter * 32 + lane;  // a warp reads its quarter of tensor memory
+        parts([&](int n, int tile, int group, int, int) {
+            const int count = off[group + 1] - (off[group] + (tile - tiles[group]) * kShRows);
+            const bool ok = mbar_wait_own(smem_u32(&made[n & 1]), (n >> 1) & 1, p.status, kSiteLoraDone, p.wait_ns);
+            if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+            tc_fence_after();
+            float *dst = p.part + ((int64_t)(me + tile) * kShRows + row) * R;
+            const uint32_t from = tmem + (n & 1) * R + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll
             for (int c = 0; c < R; c += 16) {
                 uint32_t v[16];
-                tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
+                tmem_ld16(from + c, v);
                 tmem_ld_wait();
+                if (row < count)
 #pragma unroll
-                for (int e = 0; e < 16; e += 4)
-                    *reinterpret_cast<float4 *>(row + c + e) =
-                        make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<uint4 *>(dst + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
             }
-        }
+            tc_fence_before();
+            mbar_arrive(smem_u32(&taken[n & 1]));
+            return true;
+        });
         tc_fence_before();
-        cluster_sync();
-        tc_fence_after();  // the next tile's products overwrite the accumulator
-        if (warp < 4 && ok) {
-            // split threads per row, each with every split-th group of 4 columns
-            const int per = kShRows / split, mine = (int)threadIdx.x / split, sub = (int)threadIdx.x % split;
-            const int row = (int)sub_rank * per + mine;
-            constexpr int kGroups = R / 4;
-            float top = 0.0f;
-            float *own = part + row * C::kLd;  // this row's part here is only read by its own threads from now on
-            for (int c = sub; c < kGroups; c += split) {
-                float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                float4 v[kLoraCluster];  // all in flight
-#pragma unroll
-                for (uint32_t z = 0; z < kLoraCluster; ++z)
-                    v[z] = z < (uint32_t)split ? ld_cluster_f4(mapa_shared(smem_u32(own + 4 * c), lead + z)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int z = 0; z < kLoraCluster; ++z) {  // added in rank order
-                    a.x += v[z].x;
-                    a.y += v[z].y;
-                    a.z += v[z].z;
-                    a.w += v[z].w;
-                }
-                // the columns behind the rank belong to another adapter
-                if (4 * c >= p.rank) a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                *reinterpret_cast<float4 *>(own + 4 * c) = a;
-                top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(a.z), fabsf(a.w)));
-            }
-            for (int o = 1; o < split; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            int e = (int)(__float_as_uint(top) >> 23) - 127;
-            e = e < -100 ? -100 : e > 126 ? 0 : e;
-            const float down = pow2f(-e);
-            if (row < count) {
-                T *h = static_cast<T *>(p.h) + (int64_t)(first + row) * 2 * R;
-                for (int c = sub; c < kGroups; c += split) {
-                    const float4 a = *reinterpret_cast<const float4 *>(own + 4 * c);
-                    const float v[4] = {a.x * down, a.y * down, a.z * down, a.w * down};
-                    T hi[4], lo[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        hi[j] = narrow<T>(v[j]);
-                        lo[j] = narrow<T>(v[j] - widen(hi[j]));
-                    }
-                    memcpy(h + 4 * c, hi, 8);
-                    memcpy(h + R + 4 * c, lo, 8);
-                }
-                if (sub == 0) p.hscale[first + row] = pow2f(e);
-            }
-        }
-        fence_proxy_async();  // the next tile's copies overwrite the parts
-        cluster_sync();       // once no other CTA reads this one's
-        used += b1 - b0;
     }
+    __syncthreads();
+    tc_fence_after();
     if (warp == 5) tmem_dealloc(tmem, C::kTmem);
 }
 
@@ -744,12 +724,12 @@ __global__ void __launch_bounds__(kLoraThreads, kExPerSm<NB>) lora_expand_kernel
     constexpr int R = 8 * NB, kLd = kHLd<NB>;
     extern __shared__ __align__(16) uint8_t ahead[];
     __shared__ __align__(16) uint16_t hh[kExRows * kLd], hl[kExRows * kLd];
-    __shared__ int32_t off[kGroupsMax + 1], tiles[kGroupsMax + 1];
-    __shared__ int32_t row_s[kExRows];
+    __shared__ int32_t off[kGroupsMax + 1], tiles[kGroupsMax + 1], sh_tiles[kGroupsMax + 1];
+    __shared__ int32_t row_s[kExRows], part_s[2];
     __shared__ float scale_s[kExRows];
     // This launch starts when every CTA of the first has passed its own wait,
     // so all that came before the first (routing, base, weights) is there;
-    // only h and its scales, the first launch's results, need the wait below.
+    // only the parts of h, the first launch's results, need the wait below.
     if (p.base != p.out) copy_bare_rows<T>(p);
     for (int i = threadIdx.x; i <= p.groups; i += kLoraThreads) off[i] = p.offsets[i];
     __syncthreads();
@@ -757,6 +737,8 @@ __global__ void __launch_bounds__(kLoraThreads, kExPerSm<NB>) lora_expand_kernel
     if (threadIdx.x < 32) {
         const bool ok = build_tiles(off, p.groups, p.m, kExRows, tiles);
         if (threadIdx.x == 0) table_ok = ok;
+    } else if (threadIdx.x < 64) {
+        (void)build_tiles(off, p.groups, p.m, kShRows, sh_tiles);
     }
     __syncthreads();
     if (!table_ok) {  // reported by the first launch
@@ -782,19 +764,70 @@ __global__ void __launch_bounds__(kLoraThreads, kExPerSm<NB>) lora_expand_kernel
                 }
             }
             row_s[threadIdx.x] = r;
+        } else if (threadIdx.x == 64) {  // the tile's parts: first and number
+            const Shares share(sh_tiles[p.groups], (p.k + kShK - 1) / kShK, p.shrink_ctas);
+            const int sh_tile = sh_tiles[group] + (first - off[group]) / kShRows;
+            const int64_t step0 = (int64_t)sh_tile * share.blocks;
+            const int lo = share.owner(step0);
+            part_s[0] = lo + sh_tile;
+            part_s[1] = share.owner(step0 + share.blocks - 1) - lo + 1;
         }
         __syncthreads();
         expand_tile<T, kExRows / 16, NB>(p, group, row_s, scale_s, hh, hl, ahead, c0, c1, [&]() {
             if (!waited) griddep_wait();
             waited = true;
-            if ((int)threadIdx.x < count)
-                scale_s[threadIdx.x] = (p.scales ? p.scales[group] : 1.0f) * __ldcg(p.hscale + first + threadIdx.x);
-            const uint4 *h = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.h) + (int64_t)first * 2 * R);
-            for (int i = threadIdx.x; i < kExRows * R / 4; i += kLoraThreads) {
-                const int row = i / (R / 4), c = i % (R / 4);  // 16-byte pieces: R / 8 of each term
-                const uint4 v = row < count ? __ldcg(h + i) : make_uint4(0, 0, 0, 0);
-                uint16_t *dst = c < R / 8 ? hh + row * kLd + 8 * c : hl + row * kLd + 8 * (c - R / 8);
-                *reinterpret_cast<uint4 *>(dst) = v;
+            // h: 4 columns of a row per thread and turn, the parts added in order
+            const int n_parts = part_s[1];
+            const float *from = p.part + ((int64_t)part_s[0] * kShRows + (first - off[group]) % kShRows) * R;
+            constexpr int kLanes = R / 4, kTurns = (kExRows * kLanes + kLoraThreads - 1) / kLoraThreads;
+            constexpr int kFlight = 8 / kTurns;  // parts in flight
+            const int c = (int)threadIdx.x % kLanes, r0 = (int)threadIdx.x / kLanes;
+            float4 a[kTurns];
+#pragma unroll
+            for (int u = 0; u < kTurns; ++u) a[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int z0 = 0; z0 < n_parts; z0 += kFlight) {
+                float4 v[kFlight][kTurns];
+#pragma unroll
+                for (int z = 0; z < kFlight; ++z)
+#pragma unroll
+                    for (int u = 0; u < kTurns; ++u) {
+                        const int r = r0 + u * (kLoraThreads / kLanes);
+                        v[z][u] = z0 + z < n_parts && r < count
+                                      ? __ldcg(reinterpret_cast<const float4 *>(from + ((int64_t)(z0 + z) * kShRows + r) * R) + c)
+                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
+#pragma unroll
+                for (int z = 0; z < kFlight; ++z)
+#pragma unroll
+                    for (int u = 0; u < kTurns; ++u) {
+                        a[u].x += v[z][u].x;
+                        a[u].y += v[z][u].y;
+                        a[u].z += v[z][u].z;
+                        a[u].w += v[z][u].w;
+                    }
+            }
+            const float scale = p.scales ? p.scales[group] : 1.0f;
+#pragma unroll
+            for (int u = 0; u < kTurns; ++u) {
+                const int r = r0 + u * (kLoraThreads / kLanes);
+                // the columns behind the rank belong to another adapter
+                if (4 * c >= p.rank) a[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float top = fmaxf(fmaxf(fabsf(a[u].x), fabsf(a[u].y)), fmaxf(fabsf(a[u].z), fabsf(a[u].w)));
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                const int e = row_exponent(top);
+                const float down = pow2f(-e), f[4] = {a[u].x * down, a[u].y * down, a[u].z * down, a[u].w * down};
+                T hi[4], low[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    hi[j] = narrow<T>(f[j]);
+                    low[j] = narrow<T>(f[j] - widen(hi[j]));
+                }
+                if (r < kExRows) {
+                    memcpy(hh + r * kLd + 4 * c, hi, 8);
+                    memcpy(hl + r * kLd + 4 * c, low, 8);
+                    if (c == 0) scale_s[r] = scale * pow2f(e);
+                }
             }
             __syncthreads();
         });
@@ -804,9 +837,17 @@ __global__ void __launch_bounds__(kLoraThreads, kExPerSm<NB>) lora_expand_kernel
 }
 
 // Tiles of `rows` rows: a bound on sum ceil(rows of a group / rows).
-static int64_t tiles_bound(const LoraParams &p, int64_t rows) {
-    const int64_t t = p.m / rows + (p.groups < p.m ? p.groups : p.m);
-    return t < p.m ? t : p.m;
+static int64_t tiles_bound(int64_t m, int64_t groups, int64_t rows) {
+    const int64_t t = m / rows + (groups < m ? groups : m);
+    return t < m ? t : m;
+}
+
+// CTAs of the first launch: as many as stay on the GPU (a workspace size, so a
+// function of the shape alone).
+static int shrink_ctas(int64_t m, int64_t rank, int64_t groups) {
+    // three CTAs on an SM have 75 KB each: 73 of ring, the rest for tables
+    const int64_t stay = (rank <= 64 && groups <= 224 ? 3 : 2) * 148, most = tiles_bound(m, groups, kShRows) * kShParts;
+    return (int)(most < stay ? most : stay);
 }
 
 template <typename T, int NB>
@@ -816,19 +857,14 @@ static sharq_status lora_two(LaunchCtx &ctx, LoraParams p) {
     CUtensorMap tm_a;
     if (!make_row_map(&tm_a, p.a, (uint64_t)p.k, (uint64_t)p.groups * p.rank, (uint64_t)p.k * 2, R))
         return SHARQ_ERR_CUDA;
-    SQ_SMEM_ONCE((lora_shrink_kernel<T, R>), C::kSmem);
-    // Clusters that stay and take tiles in turn, three CTAs to an SM; their size
-    // as if every tile were full (the kernel splits a tile less where there are
-    // more).
-    const int64_t full = (p.m + kShRows - 1) / kShRows;
-    int cluster = 1;
-    while (cluster < kLoraCluster && full * cluster * 2 <= 3 * ctx.num_sms && p.k >= 2 * kShK * cluster) cluster *= 2;
-    const int64_t tiles = tiles_bound(p, kShRows), fit = 3 * ctx.num_sms / cluster;
-    sharq_status st = launch_pdl(ctx, lora_shrink_kernel<T, R>, (tiles < fit ? tiles : fit) * cluster, kShThreads, C::kSmem,
-                                 cluster, tm_a, p);
+    constexpr int kTables = 2 * (int)sizeof(int32_t);
+    SQ_SMEM_ONCE((lora_shrink_kernel<T, R>), C::kSmem + kTables * ((int)kGroupsMax + 1));
+    p.shrink_ctas = shrink_ctas(p.m, p.rank, p.groups);
+    sharq_status st = launch_pdl(ctx, lora_shrink_kernel<T, R>, p.shrink_ctas, kShThreads,
+                                 C::kSmem + kTables * (p.groups + 1), 1, tm_a, p);
     if (st != SHARQ_OK) return st;
     // CTAs that stay, unless that leaves a warp less than a block
-    const int64_t ex = tiles_bound(p, kExRows) * ((p.n + 32 * kLoraWarps - 1) / (32 * kLoraWarps));
+    const int64_t ex = tiles_bound(p.m, p.groups, kExRows) * ((p.n + 32 * kLoraWarps - 1) / (32 * kLoraWarps));
     const int64_t stay = (int64_t)kExPerSm<NB> * ctx.num_sms;
     const int64_t ctas = ex < stay ? ex : stay;
     p.bare_ctas = (int32_t)ctas;
@@ -851,14 +887,14 @@ static bool lora_many(int64_t m, int64_t rank, int64_t groups) {
 
 int64_t lora_ws_bytes(int64_t m, int64_t rank, int64_t groups) {
     if (!lora_many(m, rank, groups)) return 0;
-    return round_up(m * 4 * shrink_rank(rank), kAlign) + round_up(m * 4, kAlign);
+    return (shrink_ctas(m, rank, groups) + tiles_bound(m, groups, kShRows)) * kShRows * shrink_rank(rank) * (int64_t)sizeof(float);
 }
 
 template <typename T, int NB>
 static sharq_status lora_run(LaunchCtx &ctx, LoraParams p) {
     using C = LoraCfg<NB>;
     SQ_SMEM_ONCE((lora_kernel<T, NB>), C::kSmem);
-    const int64_t tiles = tiles_bound(p, C::kRows);
+    const int64_t tiles = tiles_bound(p.m, p.groups, C::kRows);
     // Split a tile until the CTAs fill the GPU twice, as long as a CTA keeps
     // a few hundred elements of k and of the columns.
     int cluster = 1;
@@ -891,8 +927,8 @@ sharq_status launch_lora(LaunchCtx &ctx, const void *x, int64_t ldx, int64_t m, 
                          int64_t ldo, void *ws) {
     if (m == 0) return SHARQ_OK;
     LoraParams p{x, a, b, base, scales, out, offsets, rows, slots, (int32_t)ldx, (int32_t)ldbase, (int32_t)ldo, m,
-                 (int32_t)k, (int32_t)n, (int32_t)rank, (int32_t)groups, 1, 0, ctx.status, ctx.wait_ns, ws,
-                 reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + round_up(m * 4 * shrink_rank(rank), kAlign))};
+                 (int32_t)k, (int32_t)n, (int32_t)rank, (int32_t)groups, 1, 0, ctx.status, ctx.wait_ns,
+                 static_cast<float *>(ws), 0};
     return dtype == SHARQ_F16 ? lora_any<__half>(ctx, p) : lora_any<__nv_bfloat16>(ctx, p);
 }
 

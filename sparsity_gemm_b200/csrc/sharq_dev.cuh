@@ -396,7 +396,8 @@ __device__ __forceinline__ bool mbar_wait_own(uint32_t bar, uint32_t parity, uns
 }
 
 // Wait sites of the 16/32-bit operators.
-enum : unsigned { kSiteNormRing = 0x141, kSiteLoraFull = 0x142, kSiteLoraEmpty = 0x143, kSiteLoraDone = 0x144 };
+enum : unsigned { kSiteNormRing = 0x141, kSiteLoraFull = 0x142, kSiteLoraEmpty = 0x143, kSiteLoraDone = 0x144,
+                kSiteLoraTaken = 0x145 };
 
 // ---------------------------------------------------------------------------
 // Grouped (mixture-of-experts) launches. Group g owns grouped rows
