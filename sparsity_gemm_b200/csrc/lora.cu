@@ -518,7 +518,9 @@ constexpr int kShK = 64;
 constexpr int kShThreads = 320;  // warps 0-3: copies of x; 4: copies of A; 5: products; 6-9: parts out
 constexpr int kShCopiers = 128, kShWriters = 128;
 constexpr int kShX = kShRows * kShK * 2;
-constexpr int kShParts = 8;      // CTAs per tile where there are more CTAs than that
+// CTAs per tile where there are more than that: with 4, 64 rows of rank 64 take
+// 12.9 us, with 8 10.7, with 16 10.3, but 4096 rows of 8 adapters 44.8, 45.1 and 49.4.
+constexpr int kShParts = 8;
 
 template <int R>
 struct ShrinkCfg {
@@ -875,14 +877,19 @@ static sharq_status lora_two(LaunchCtx &ctx, LoraParams p) {
 // Whether a call takes the two-launch form (and so needs a workspace), by what
 // the host knows: rows, rank and adapters (not how many of them the batch
 // uses). Measured at k = n = 4096 in fp16, one launch against two, in us:
-//   rank 16   1 adapter:   512 rows  9.5 / 12.2, 1024 16.7 / 16.1, 4096 37 / 31
-//             64 adapters: 1024     13.3 / 25.1, 4096 37 / 39
-//   rank 64   1 adapter:   16 rows  7.8 / 12.3, 64 14.4 / 12.6, 1024 42 / 21
-//             64 adapters: 512      25 / 34, 1024 31 / 37, 4096 77 / 59
+//   rank 16   1 adapter:    512 rows  8.4 / 10.0, 1024 15.3 / 14.2, 4096 35.5 / 29.1
+//             64 adapters:  2048     18.7 / 23.1, 4096 36.1 / 31.9
+//             256 adapters: 512      14.3 / 22.1, 1024 26.4 / 23.3
+//   rank 64   1 adapter:    32 rows   8.3 / 10.0, 64 14.7 / 10.5, 1024 43.1 / 19.7
+//             8 adapters:   64       13.7 / 11.3
+//             64 adapters:  512      25.9 / 28.6, 1024 31.6 / 30.7, 4096 77.4 / 52.2
+//             256 adapters: 512      28.5 / 29.8, 1024 40.0 / 32.2
 // A 16-row tile's accumulators and its reading of A and B per 16 rows cost the
-// one-launch form more the larger the rank is.
+// one-launch form more the larger the rank is; and where there could be more
+// tiles than fill the GPU twice it does not split them.
 static bool lora_many(int64_t m, int64_t rank, int64_t groups) {
-    return rank <= 32 ? m >= 1024 && m > 32 * groups : m >= 64 && m >= 16 * groups;
+    if (rank <= 32) return m >= 1024 && (m > 32 * groups || m / 16 + groups >= 2 * 148);
+    return m >= 1024 || (m >= 64 && (groups <= 8 || m >= 16 * groups));
 }
 
 int64_t lora_ws_bytes(int64_t m, int64_t rank, int64_t groups) {
