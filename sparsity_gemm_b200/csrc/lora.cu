@@ -347,11 +347,12 @@ struct LoraCfg {
     static constexpr int kRows = 16, kRank = 8 * NB;
     static constexpr int kLd = kRank + 8;   // row stride of the binary32 parts
     static constexpr int kSmem = kLoraWarps * kRows * kLd * 4 + 2 * kRows * kHLd<NB> * 2 + kAheadBytes<1>;
+    static constexpr int kPerSm = NB == 2 ? 3 : NB <= 8 ? 2 : 1;  // CTAs on an SM, by registers
     static constexpr int kStep = NB >= 8 ? 1 : 2;  // steps of 32 elements of k in flight
 };
 
 template <typename T, int NB>
-__global__ void __launch_bounds__(kLoraThreads) lora_kernel(const LoraParams p) {
+__global__ void __launch_bounds__(kLoraThreads, LoraCfg<NB>::kPerSm) lora_kernel(const LoraParams p) {
     using C = LoraCfg<NB>;
     extern __shared__ __align__(16) uint8_t smem[];
     float *part = reinterpret_cast<float *>(smem);  // [warps][rows][kLd]; [0]: the CTA's sum
@@ -877,19 +878,19 @@ static sharq_status lora_two(LaunchCtx &ctx, LoraParams p) {
 // Whether a call takes the two-launch form (and so needs a workspace), by what
 // the host knows: rows, rank and adapters (not how many of them the batch
 // uses). Measured at k = n = 4096 in fp16, one launch against two, in us:
-//   rank 16   1 adapter:    512 rows  8.4 / 10.0, 1024 15.3 / 14.2, 4096 35.5 / 29.1
-//             64 adapters:  2048     18.7 / 23.1, 4096 36.1 / 31.9
-//             256 adapters: 512      14.3 / 22.1, 1024 26.4 / 23.3
-//   rank 64   1 adapter:    32 rows   8.3 / 10.0, 64 14.7 / 10.5, 1024 43.1 / 19.7
-//             8 adapters:   64       13.7 / 11.3
-//             64 adapters:  512      25.9 / 28.6, 1024 31.6 / 30.7, 4096 77.4 / 52.2
-//             256 adapters: 512      28.5 / 29.8, 1024 40.0 / 32.2
-// A 16-row tile's accumulators and its reading of A and B per 16 rows cost the
-// one-launch form more the larger the rank is; and where there could be more
-// tiles than fill the GPU twice it does not split them.
+//   rank 16   1 adapter:           1024 rows 12 / 14, 3000 22 / 23, 4096 40 / 29
+//             64 adapters:         1024 13 / 21, 3000 24 / 27, 4096 41 / 32
+//   rank 32   1 adapter:           2048 18 / 22, 3000 34 / 26; 64: 2048 20 / 26, 3000 38 / 32
+//   rank 64   1 adapter:           64 10 / 11, 1024 17 / 19, 1500 29 / 23, 4096 58 / 44
+//             64 adapters:         64 17 / 26, 1024 23 / 31, 1500 38 / 33
+//             64 used of 256:      64 19 / 28, 256 31 / 29, 1024 38 / 32
+//   rank 128  1 adapter:           1024 26 / 28, 1500 50 / 34
+//             100 used of 256:     128 74 / 65, 1024 80 / 70
+// One launch leads as long as its 16-row tiles fit on the GPU at once; their
+// accumulators and reading A and B per 16 rows cost more the larger the rank is.
 static bool lora_many(int64_t m, int64_t rank, int64_t groups) {
-    if (rank <= 32) return m >= 1024 && (m > 32 * groups || m / 16 + groups >= 2 * 148);
-    return m >= 1024 || (m >= 64 && (groups <= 8 || m >= 16 * groups));
+    if (rank <= 32) return m >= (rank <= 16 ? 3500 : 2500);
+    return m > 1024 || (m >= 128 && groups > 148);
 }
 
 int64_t lora_ws_bytes(int64_t m, int64_t rank, int64_t groups) {
@@ -902,12 +903,22 @@ static sharq_status lora_run(LaunchCtx &ctx, LoraParams p) {
     using C = LoraCfg<NB>;
     SQ_SMEM_ONCE((lora_kernel<T, NB>), C::kSmem);
     const int64_t tiles = tiles_bound(p.m, p.groups, C::kRows);
-    // Split a tile until the CTAs fill the GPU twice, as long as a CTA keeps
-    // a few hundred elements of k and of the columns.
+    // Split a tile as long as the CTAs fit on the GPU together (clusters of 8 leave
+    // a part of it empty) and keep a few hundred elements of k and of the columns.
+    // How many tiles there are is only known on the device: the guess is that every
+    // group is used and most of them fill their last tile. A second wave costs the
+    // most: 64 rows of 64 adapters, rank 64, take 17 us with 256 CTAs, 35 with 512
+    // that do not fit. A tile split in two whatever the guess helps where few of
+    // the adapters are used (256 rows, rank 16, one of 256: 12.7 us, 19.4 without).
+    const int64_t guess = p.m >= 16 * p.groups ? p.m / 16 + p.groups / 8 : p.groups < p.m ? p.groups : p.m;
+    const int64_t sms = ctx.num_sms, slots = C::kPerSm * sms, eights = slots * 3 / 4;
     int cluster = 1;
-    while (cluster < kLoraCluster && tiles * cluster < 2 * ctx.num_sms && p.k >= 512 * cluster) cluster *= 2;
+    while (cluster < kLoraCluster && p.k >= 512 * cluster &&
+           (2 * guess * cluster <= (2 * cluster == 8 ? eights : slots) || (cluster == 1 && guess < 2 * sms)))
+        cluster *= 2;
     p.nsplit = 1;
-    while (p.nsplit < 16 && tiles * cluster * p.nsplit < ctx.num_sms && p.n >= 256 * cluster * p.nsplit) p.nsplit *= 2;
+    const int64_t wide = eights < 2 * sms ? eights : 2 * sms;
+    while (p.nsplit < 16 && 2 * guess * cluster * p.nsplit <= wide && p.n >= 256 * cluster * p.nsplit) p.nsplit *= 2;
     p.bare_ctas = (int32_t)round_up(bare_ctas(ctx, p), cluster);
     return launch_pdl(ctx, lora_kernel<T, NB>, p.bare_ctas + tiles * cluster * p.nsplit, kLoraThreads, C::kSmem, cluster, p);
 }

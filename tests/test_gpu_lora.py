@@ -73,7 +73,9 @@ SHAPES = [(1, 256, 256, 16, 1), (1, 4096, 14336, 64, 3), (2, 8, 8, 8, 1), (5, 26
           (65, 256, 256, 16, 1), (129, 304, 96, 48, 2), (300, 512, 512, 64, 3), (300, 512, 520, 72, 3), (200, 640, 640, 128, 2),
           (40, 640, 640, 120, 40), (1000, 256, 512, 16, 1), (1000, 384, 320, 32, 7), (777, 512, 256, 64, 100),
           (500, 256, 256, 8, 1024), (4099, 256, 264, 56, 5), (1100, 256, 264, 16, 2), (2100, 328, 512, 32, 5),
-          (1500, 136, 200, 8, 1), (64, 4096, 256, 96, 1), (70000, 64, 32, 64, 3), (20000, 72, 40, 40, 1000)]
+          (1500, 136, 200, 8, 1), (64, 4096, 256, 96, 1), (70000, 64, 32, 64, 3), (20000, 72, 40, 40, 1000),
+          (2600, 328, 512, 32, 5), (2700, 136, 200, 24, 3), (1100, 256, 264, 72, 2), (1300, 520, 328, 120, 3),
+          (3600, 256, 264, 16, 2), (3500, 8, 8, 8, 1), (130, 256, 264, 64, 200)]
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))

@@ -125,7 +125,7 @@ def test_two_graphs_of_one_pool():
     assert sq.get_last_error() == sq.OK
 
 
-@pytest.mark.parametrize("m,rank,groups", [(96, 64, 3), (1100, 16, 5), (40, 16, 3)])
+@pytest.mark.parametrize("m,rank,groups", [(96, 64, 3), (1100, 16, 5), (40, 16, 3), (1100, 64, 3), (130, 64, 160)])
 def test_inputs_changed_right_before_a_call(m, rank, groups):
     """Weights, adapters' ids, base and statistics that a small kernel rewrites
     in place right before each call (the next one's first loads may already be
