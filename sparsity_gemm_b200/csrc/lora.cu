@@ -351,8 +351,8 @@ struct LoraCfg {
     static constexpr int kStep = NB >= 8 ? 1 : 2;  // steps of 32 elements of k in flight
 };
 
-template <typename T, int NB>
-__global__ void __launch_bounds__(kLoraThreads, LoraCfg<NB>::kPerSm) lora_kernel(const LoraParams p) {
+template <typename T, int NB, int PER_SM>
+__global__ void __launch_bounds__(kLoraThreads, PER_SM) lora_kernel(const LoraParams p) {
     using C = LoraCfg<NB>;
     extern __shared__ __align__(16) uint8_t smem[];
     float *part = reinterpret_cast<float *>(smem);  // [warps][rows][kLd]; [0]: the CTA's sum
@@ -901,7 +901,6 @@ int64_t lora_ws_bytes(int64_t m, int64_t rank, int64_t groups) {
 template <typename T, int NB>
 static sharq_status lora_run(LaunchCtx &ctx, LoraParams p) {
     using C = LoraCfg<NB>;
-    SQ_SMEM_ONCE((lora_kernel<T, NB>), C::kSmem);
     const int64_t tiles = tiles_bound(p.m, p.groups, C::kRows);
     // Split a tile as long as the CTAs fit on the GPU together (clusters of 8 leave
     // a part of it empty) and keep a few hundred elements of k and of the columns.
@@ -920,7 +919,17 @@ static sharq_status lora_run(LaunchCtx &ctx, LoraParams p) {
     const int64_t wide = eights < 2 * sms ? eights : 2 * sms;
     while (p.nsplit < 16 && 2 * guess * cluster * p.nsplit <= wide && p.n >= 256 * cluster * p.nsplit) p.nsplit *= 2;
     p.bare_ctas = (int32_t)round_up(bare_ctas(ctx, p), cluster);
-    return launch_pdl(ctx, lora_kernel<T, NB>, p.bare_ctas + tiles * cluster * p.nsplit, kLoraThreads, C::kSmem, cluster, p);
+    const int64_t ctas = p.bare_ctas + tiles * cluster * p.nsplit;
+    // rank 33 to 64: two CTAs on an SM leave too few registers; where one per SM is
+    // all there is they keep theirs (one row of rank 64: 6.1 us against 6.7)
+    if constexpr (NB == 8) {
+        if (ctas <= sms) {
+            SQ_SMEM_ONCE((lora_kernel<T, NB, 1>), C::kSmem);
+            return launch_pdl(ctx, lora_kernel<T, NB, 1>, ctas, kLoraThreads, C::kSmem, cluster, p);
+        }
+    }
+    SQ_SMEM_ONCE((lora_kernel<T, NB, C::kPerSm>), C::kSmem);
+    return launch_pdl(ctx, lora_kernel<T, NB, C::kPerSm>, ctas, kLoraThreads, C::kSmem, cluster, p);
 }
 
 template <typename T>
