@@ -643,7 +643,7 @@ sharq_status sharq_combine_backward(const void *dout_dev, const void *y_dev, int
  * Invalid offsets leave the groups' rows unwritten, invalid rows are skipped; both are reported
  * by sharq_get_last_error as SHARQ_ERR_INVALID_ARG.
  *   ws_dev    workspace of sharq_lora_bytes(m_tok, rank, n_groups) bytes,
- *             256-byte aligned; NULL where that is 0 (few rows per adapter).
+ *             256-byte aligned; NULL where that is 0 (few rows).
  */
 size_t sharq_lora_bytes(int64_t m_tok, int64_t rank, int64_t n_groups);
 sharq_status sharq_lora(const void *x_dev, int64_t ldx, int64_t m_tok, int64_t k, const void *a_dev, const void *b_dev,

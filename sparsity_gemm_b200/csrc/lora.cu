@@ -715,7 +715,9 @@ __global__ void __launch_bounds__(kShThreads, ShrinkCfg<R>::kPerSm)
 // Tiles of 32 rows: 64 rows halve what is read of B (from L2) but leave two
 // CTAs of registers on an SM; 8192 x 4096, rank 16: 33.6 us against 30.0, 4099
 // x 4096, rank 64, 64 adapters: 40.2 against 33.5. More CTAs than these take
-// the L1 that B's lines need: with four, 32.5 and 35.8 us.
+// the L1 that B's lines need: with four, 32.5 and 35.8 us; so does fetching B ahead
+// into shared memory (rank 64: 39 us against 33.6), and more of base in flight
+// changes nothing.
 constexpr int kExRows = 32;
 template <int NB>
 constexpr int kExPerSm = NB <= 4 ? 3 : 2;

@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
 // ahead. The barrier of a row's reduction also frees its ring slot. Bound by
 // instructions and their latency (half the issue slots at 16 warps per SM;
 // fewer columns per thread and more warps measured slower: 8192 x 4096 in bf16
-// takes 37 us like this, 56 with 8 columns): 73% of the copy rate with the
+// takes 36.5 us like this, 56 with 8 columns): 75% of the copy rate with the
 // reduction of the partial rows.
 constexpr int kRingMax = 8;            // most rows in a ring
 constexpr int kRingBytes = 160 << 10;  // shared memory of an SM's rings
