@@ -634,8 +634,9 @@ sharq_status sharq_combine_backward(const void *dout_dev, const void *y_dev, int
  *   base_dev  [m_tok][n_out], row stride ldbase, or NULL (zero).
  *   out_dev   [m_tok][n_out], row stride ldo; may be base_dev itself (ldo ==
  *             ldbase), then rows without a group are left alone.
- * The product x A^T is kept in binary32 (each row as two 16-bit terms for the
- * second product), accumulation is binary32, the sum is rounded once.
+ * The product x A^T is binary32 (for the second product three bf16 terms, which
+ * hold all of it, or two fp16 terms, within 2^-23 of the value), accumulation is
+ * binary32, the sum is rounded once.
  * dtype is SHARQ_F16 or SHARQ_BF16. k, n_out, rank and the row strides are
  * multiples of 8, buffers 16-byte aligned; rank <= SHARQ_RANK_MAX, n_out <=
  * 2^20, n_groups <= SHARQ_GROUPS_MAX. Column slices of one buffer are fine as

@@ -21,9 +21,11 @@
 // consecutive columns.
 //
 // h is binary32. For the second product each row is scaled by a power of two
-// and split into two 16-bit terms (the rounded value and the rounded rest),
-// which keeps 2^-16 (bf16) or 2^-22 (fp16) of the row's largest value instead
-// of 2^-8 or 2^-11: the only rounding that shows is the output's own.
+// and split into 16-bit terms, each the rounded rest of those before it. Three
+// bf16 terms hold all 24 bits of a value. Two fp16 terms hold 23 (within 2^-23
+// of the value; of values below 2^-16 of the row's largest, within 2^-39 of that
+// largest): a third would add a half to the second product's instructions for
+// one bit, far below what the sums of both products round away.
 #include <cuda_runtime.h>
 
 #include "sharq_dev.cuh"
@@ -81,10 +83,28 @@ __device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) { return __uint_as_float(ld_cluster_u32(addr)); }
 
-// The power of two that brings a row's largest value to [1, 2).
+// The terms of h, and the power of two that the row's largest value is brought
+// to: near fp16's largest, so that the second terms of small values stay above
+// its smallest (bf16 has binary32's range).
+template <typename T>
+constexpr int kTerms = IsBf16<T>::v ? 3 : 2;
+template <typename T>
+constexpr int kTopExponent = IsBf16<T>::v ? 0 : 14;
+
+// The exponent of the power of two that a row is divided by.
+template <typename T>
 __device__ __forceinline__ int row_exponent(float top) {
-    const int e = (int)(__float_as_uint(top) >> 23) - 127;
+    const int e = (int)(__float_as_uint(top) >> 23) - 127 - kTopExponent<T>;
     return e < -100 ? -100 : e > 126 ? 0 : e;
+}
+
+template <typename T>
+__device__ __forceinline__ void split_terms(float v, T (&t)[kTerms<T>]) {
+#pragma unroll
+    for (int z = 0; z < kTerms<T>; ++z) {
+        t[z] = narrow<T>(v);
+        v -= widen(t[z]);  // exact
+    }
 }
 
 // The tile's group and rows, found by warp 0 in the offsets. tile_s: [0] group
@@ -167,14 +187,14 @@ __device__ __forceinline__ void cta_find_tile(const LoraParams &p, int32_t *off,
 }
 
 // out = base + scale h B^T for the tile's rows, over the blocks c0 .. c1-1 of 32
-// columns; warps take turns. hh, hl: the two terms of h.
+// columns; warps take turns. terms: those of h, term_ld elements apart.
 // A lane reads base for the very elements it writes, so the next blocks' are on
 // their way into `ahead` (written and read by that thread alone) while a block
 // is computed; B's part of the next block is on its way into registers. ready()
 // runs after the first of these loads and before h is read.
 constexpr int kAhead = 2;
 
-// Row stride of the two terms of h: a lane of a quarter-warp reads 16 bytes of
+// Row stride of a term of h: a lane of a quarter-warp reads 16 bytes of
 // one of two rows, 64 bytes of each (rank up to 16: a half-warp 8 bytes of one of
 // four rows), and these fill the 32 banks.
 template <int NB>
@@ -185,7 +205,7 @@ constexpr int kAheadBytes = kAhead * 2 * MT * 16 * kLoraThreads;
 
 template <typename T, int MT, int NB, typename F>
 __device__ __forceinline__ void expand_tile(const LoraParams &p, int group, const int32_t *row_s, const float *scale_s,
-                                            const uint16_t *hh, const uint16_t *hl, uint8_t *ahead, int c0, int c1,
+                                            const uint16_t *terms, int term_ld, uint8_t *ahead, int c0, int c1,
                                             F ready) {
     constexpr int kLd = kHLd<NB>, kS = (NB + 3) / 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
@@ -260,8 +280,8 @@ __device__ __forceinline__ void expand_tile(const LoraParams &p, int group, cons
         for (int i = 0; i < MT; ++i) {
             float d[4][4];
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                const uint16_t *hp = (z ? hl : hh) + (16 * i + g8) * kLd;
+            for (int z = 0; z < kTerms<T>; ++z) {
+                const uint16_t *hp = terms + z * term_ld + (16 * i + g8) * kLd;
 #pragma unroll
                 for (int s = 0; s < kS; ++s) {
                     if (NB == 2) {
@@ -342,22 +362,22 @@ static int bare_ctas(const LaunchCtx &ctx, const LoraParams &p) {
 
 // NB: 8-column blocks of the padded rank.
 constexpr int kLoraCluster = 8;  // most CTAs of a tile
-template <int NB>
+template <typename T, int NB>
 struct LoraCfg {
     static constexpr int kRows = 16, kRank = 8 * NB;
     static constexpr int kLd = kRank + 8;   // row stride of the binary32 parts
-    static constexpr int kSmem = kLoraWarps * kRows * kLd * 4 + 2 * kRows * kHLd<NB> * 2 + kAheadBytes<1>;
+    static constexpr int kTermLd = kRows * kHLd<NB>;
+    static constexpr int kSmem = kLoraWarps * kRows * kLd * 4 + kTerms<T> * kTermLd * 2 + kAheadBytes<1>;
     static constexpr int kPerSm = NB == 2 ? 3 : NB <= 8 ? 2 : 1;  // CTAs on an SM, by registers
     static constexpr int kStep = NB >= 8 ? 1 : 2;  // steps of 32 elements of k in flight
 };
 
 template <typename T, int NB, int PER_SM>
 __global__ void __launch_bounds__(kLoraThreads, PER_SM) lora_kernel(const LoraParams p) {
-    using C = LoraCfg<NB>;
+    using C = LoraCfg<T, NB>;
     extern __shared__ __align__(16) uint8_t smem[];
     float *part = reinterpret_cast<float *>(smem);  // [warps][rows][kLd]; [0]: the CTA's sum
-    uint16_t *hh = reinterpret_cast<uint16_t *>(smem + kLoraWarps * C::kRows * C::kLd * 4);  // [rows][kHLd]
-    uint16_t *hl = hh + C::kRows * kHLd<NB>;
+    uint16_t *terms = reinterpret_cast<uint16_t *>(smem + kLoraWarps * C::kRows * C::kLd * 4);  // [terms][rows][kHLd]
     __shared__ int32_t off[kGroupsMax + 1];
     __shared__ int32_t tile_s[3];
     __shared__ int32_t row_s[C::kRows];
@@ -472,17 +492,16 @@ __global__ void __launch_bounds__(kLoraThreads, PER_SM) lora_kernel(const LoraPa
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                const int e = row_exponent(top);
+                const int e = row_exponent<T>(top);
                 const float down = pow2f(-e), up = pow2f(e);
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
                     const int c = i * 32 + lane;
                     if (c < C::kRank) {
-                        const float v = h[i] * down;
-                        const T hi = narrow<T>(v);
-                        const T lo = narrow<T>(v - widen(hi));
-                        memcpy(hh + r * kHLd<NB> + c, &hi, 2);
-                        memcpy(hl + r * kHLd<NB> + c, &lo, 2);
+                        T t[kTerms<T>];
+                        split_terms(h[i] * down, t);
+#pragma unroll
+                        for (int z = 0; z < kTerms<T>; ++z) memcpy(terms + z * C::kTermLd + r * kHLd<NB> + c, &t[z], 2);
                     }
                 }
                 if (lane == 0) scale_s[r] = scale * up;
@@ -494,7 +513,7 @@ __global__ void __launch_bounds__(kLoraThreads, PER_SM) lora_kernel(const LoraPa
 
         const int64_t piece = (int64_t)part_n * csize + crank, pieces = (int64_t)p.nsplit * csize;
         const int blocks = (p.n + 31) / 32;
-        expand_tile<T, 1, NB>(p, group, row_s, scale_s, hh, hl, smem + C::kSmem - kAheadBytes<1>,
+        expand_tile<T, 1, NB>(p, group, row_s, scale_s, terms, C::kTermLd, smem + C::kSmem - kAheadBytes<1>,
                                (int)(blocks * piece / pieces), (int)(blocks * (piece + 1) / pieces), make_h);
         cluster_wait();  // no CTA leaves while another reads its part
     }
@@ -717,7 +736,8 @@ __global__ void __launch_bounds__(kShThreads, ShrinkCfg<R>::kPerSm)
 // x 4096, rank 64, 64 adapters: 40.2 against 33.5. More CTAs than these take
 // the L1 that B's lines need: with four, 32.5 and 35.8 us; so does fetching B ahead
 // into shared memory (rank 64: 39 us against 33.6), and more of base in flight
-// changes nothing.
+// changes nothing. (Rank 64 in bf16, measured with two terms of h; the third
+// takes 3.5 us more.)
 constexpr int kExRows = 32;
 template <int NB>
 constexpr int kExPerSm = NB <= 4 ? 3 : 2;
@@ -728,7 +748,7 @@ template <typename T, int NB>
 __global__ void __launch_bounds__(kLoraThreads, kExPerSm<NB>) lora_expand_kernel(const LoraParams p) {
     constexpr int R = 8 * NB, kLd = kHLd<NB>;
     extern __shared__ __align__(16) uint8_t ahead[];
-    __shared__ __align__(16) uint16_t hh[kExRows * kLd], hl[kExRows * kLd];
+    __shared__ __align__(16) uint16_t terms[kTerms<T>][kExRows * kLd];
     __shared__ int32_t off[kGroupsMax + 1], tiles[kGroupsMax + 1], sh_tiles[kGroupsMax + 1];
     __shared__ int32_t row_s[kExRows], part_s[2];
     __shared__ float scale_s[kExRows];
@@ -778,7 +798,7 @@ __global__ void __launch_bounds__(kLoraThreads, kExPerSm<NB>) lora_expand_kernel
             part_s[1] = share.owner(step0 + share.blocks - 1) - lo + 1;
         }
         __syncthreads();
-        expand_tile<T, kExRows / 16, NB>(p, group, row_s, scale_s, hh, hl, ahead, c0, c1, [&]() {
+        expand_tile<T, kExRows / 16, NB>(p, group, row_s, scale_s, terms[0], kExRows * kLd, ahead, c0, c1, [&]() {
             if (!waited) griddep_wait();
             waited = true;
             // h: 4 columns of a row per thread and turn, the parts added in order
@@ -820,17 +840,17 @@ __global__ void __launch_bounds__(kLoraThreads, kExPerSm<NB>) lora_expand_kernel
                 float top = fmaxf(fmaxf(fabsf(a[u].x), fabsf(a[u].y)), fmaxf(fabsf(a[u].z), fabsf(a[u].w)));
 #pragma unroll
                 for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                const int e = row_exponent(top);
+                const int e = row_exponent<T>(top);
                 const float down = pow2f(-e), f[4] = {a[u].x * down, a[u].y * down, a[u].z * down, a[u].w * down};
-                T hi[4], low[4];
+                T t[4][kTerms<T>];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    hi[j] = narrow<T>(f[j]);
-                    low[j] = narrow<T>(f[j] - widen(hi[j]));
-                }
+                for (int j = 0; j < 4; ++j) split_terms(f[j], t[j]);
                 if (r < kExRows) {
-                    memcpy(hh + r * kLd + 4 * c, hi, 8);
-                    memcpy(hl + r * kLd + 4 * c, low, 8);
+#pragma unroll
+                    for (int z = 0; z < kTerms<T>; ++z) {
+                        const T four[4] = {t[0][z], t[1][z], t[2][z], t[3][z]};
+                        memcpy(terms[z] + r * kLd + 4 * c, four, 8);
+                    }
                     if (c == 0) scale_s[r] = scale * pow2f(e);
                 }
             }
@@ -902,7 +922,7 @@ int64_t lora_ws_bytes(int64_t m, int64_t rank, int64_t groups) {
 
 template <typename T, int NB>
 static sharq_status lora_run(LaunchCtx &ctx, LoraParams p) {
-    using C = LoraCfg<NB>;
+    using C = LoraCfg<T, NB>;
     const int64_t tiles = tiles_bound(p.m, p.groups, C::kRows);
     // Split a tile as long as the CTAs fit on the GPU together (clusters of 8 leave
     // a part of it empty) and keep a few hundred elements of k and of the columns.
