@@ -536,8 +536,10 @@ typedef enum sharq_dtype {
  *   mean_dev, rstd_dev  float [m_tok] for the backward pass, or NULL (mean_dev
  *                       is NULL for RMSNorm).
  *   eps                 finite and > 0.
- * The statistics are binary32 sums, the variance around the mean. They are
- * not the exact statistics of sharq_prepare, which differ in the last bits.
+ * The statistics are binary32 sums, the variance around the mean; y is taken
+ * around a mean of more digits than mean_dev holds. They are not the exact
+ * statistics of sharq_prepare, which differ in the last bits. Rows whose squares
+ * pass binary32's range (values above about 1e19) give rstd = 0.
  */
 sharq_status sharq_layer_norm(const void *x_dev, int64_t m_tok, int64_t k, const void *ln_w_dev, const void *ln_b_dev,
                               float eps, int norm, int dtype, void *y_dev, float *mean_dev, float *rstd_dev,
