@@ -554,6 +554,7 @@ sharq_status sharq_layer_norm(const void *x_dev, int64_t m_tok, int64_t k, const
  *                       RMSNorm).
  *   dx_dev              [m_tok][k] of the element type; may be dy_dev itself.
  *   dw_dev, db_dev      float [k], or NULL; written (zero) for m_tok == 0 too.
+ *                       db_dev is NULL for RMSNorm, which has no ln_b.
  *   ws_dev              workspace of sharq_layer_norm_backward_bytes(m_tok, k)
  *                       bytes, 256-byte aligned; may be NULL where dw and db
  *                       are NULL and k <= 8192 (longer rows take two passes).

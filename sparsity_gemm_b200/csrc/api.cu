@@ -643,7 +643,7 @@ sharq_status sharq_layer_norm_backward(const void *dy_dev, const void *x_dev, in
                                        size_t ws_bytes, void *stream) {
     g_last_launches = 0;
     if (!dtype_ok(dtype) || !rows_ok(m_tok) || !width_ok(k)) return SHARQ_ERR_INVALID_ARG;
-    if ((norm != 0 && norm != 1) || (norm == 1 && mean_dev)) return SHARQ_ERR_INVALID_ARG;
+    if ((norm != 0 && norm != 1) || (norm == 1 && (mean_dev || db_dev))) return SHARQ_ERR_INVALID_ARG;
     const int64_t e = dtype_bytes(dtype), bytes = m_tok * k * e;
     if (m_tok > 0) {
         if (!dy_dev || !x_dev || !dx_dev || !rstd_dev || (norm == 0 && !mean_dev)) return SHARQ_ERR_INVALID_ARG;
