@@ -639,7 +639,8 @@ sharq_status sharq_combine_backward(const void *dout_dev, const void *y_dev, int
  *             ldbase), then rows without a group are left alone.
  * The product x A^T is binary32 (for the second product three bf16 terms, which
  * hold all of it, or two fp16 terms, within 2^-23 of the value), accumulation is
- * binary32, the sum is rounded once.
+ * binary32, the sum is rounded once. Infinities and NaN in x or A come out as in
+ * the formula; b_dev must be finite (an infinity there makes its column NaN).
  * dtype is SHARQ_F16 or SHARQ_BF16. k, n_out, rank and the row strides are
  * multiples of 8, buffers 16-byte aligned; rank <= SHARQ_RANK_MAX, n_out <=
  * 2^20, n_groups <= SHARQ_GROUPS_MAX. Column slices of one buffer are fine as

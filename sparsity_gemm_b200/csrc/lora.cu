@@ -91,19 +91,28 @@ constexpr int kTerms = IsBf16<T>::v ? 3 : 2;
 template <typename T>
 constexpr int kTopExponent = IsBf16<T>::v ? 0 : 14;
 
-// The exponent of the power of two that a row is divided by.
+// The magnitude of a value as far as it counts for its row's scale.
+__device__ __forceinline__ float finite_abs(float v) {
+    const float a = fabsf(v);
+    return a <= 3.4028235e38f ? a : 0.0f;
+}
+
+// The exponent of the power of two that a row is divided by; top: its largest
+// finite magnitude.
 template <typename T>
 __device__ __forceinline__ int row_exponent(float top) {
     const int e = (int)(__float_as_uint(top) >> 23) - 127 - kTopExponent<T>;
-    return e < -100 ? -100 : e > 126 ? 0 : e;
+    return e < -100 ? -100 : e > 126 ? 126 : e;
 }
 
+// An infinity or a NaN is its first term, with nothing left for the others.
 template <typename T>
 __device__ __forceinline__ void split_terms(float v, T (&t)[kTerms<T>]) {
 #pragma unroll
     for (int z = 0; z < kTerms<T>; ++z) {
         t[z] = narrow<T>(v);
         v -= widen(t[z]);  // exact
+        if (v != v) v = 0.0f;
     }
 }
 
@@ -487,8 +496,8 @@ __global__ void __launch_bounds__(kLoraThreads, PER_SM) lora_kernel(const LoraPa
                     h[i] = 0.0f;
 #pragma unroll
                     for (uint32_t z = 0; z < kLoraCluster; ++z) h[i] += v[z];
-                    if (c >= C::kRank) h[i] = 0.0f;
-                    top = fmaxf(top, fabsf(h[i]));
+                    if (c >= p.rank) h[i] = 0.0f;  // an infinity in x makes NaN of the padding's zeros
+                    top = fmaxf(top, finite_abs(h[i]));
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
@@ -837,7 +846,7 @@ __global__ void __launch_bounds__(kLoraThreads, kExPerSm<NB>) lora_expand_kernel
                 const int r = r0 + u * (kLoraThreads / kLanes);
                 // the columns behind the rank belong to another adapter
                 if (4 * c >= p.rank) a[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                float top = fmaxf(fmaxf(fabsf(a[u].x), fabsf(a[u].y)), fmaxf(fabsf(a[u].z), fabsf(a[u].w)));
+                float top = fmaxf(fmaxf(finite_abs(a[u].x), finite_abs(a[u].y)), fmaxf(finite_abs(a[u].z), finite_abs(a[u].w)));
 #pragma unroll
                 for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
                 const int e = row_exponent<T>(top);

@@ -43,3 +43,68 @@ def test_products_keep_the_digits_of_binary32(m, rank, dt, big):
     r = sq.route(torch.zeros(m, dtype=torch.int32, device="cuda"), 1)
     assert torch.equal(sq.lora(x, a, b, r), want)
     assert sq.get_last_error() == sq.OK
+
+
+def _formula(x, a, b):
+    """x A^T B^T of one adapter in binary64, term by term (0 times infinity is
+    NaN, and nothing else is)."""
+    h = (x.double().unsqueeze(1) * a.double()).sum(2)
+    return (h.unsqueeze(1) * b.double()).sum(2)
+
+
+def _same(got, want, tol):
+    nan, inf = want.isnan(), want.isinf()
+    assert torch.equal(got.isnan(), nan)
+    assert torch.equal(got[inf].double(), want[inf])
+    fine = ~nan & ~inf
+    assert bool(((got.double() - want).abs()[fine] <= tol * want.abs().clamp_min(1.0)[fine]).all())
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("m,rank", FORMS)
+def test_infinities_come_out_as_in_the_formula(m, rank, dt):
+    """An infinite x makes every column of its row infinite (by the signs of A
+    and B) or NaN, an infinite A the columns of its adapter's rows; other rows,
+    and the rows of an adapter beside one of NaN, are as they were. Tolerance:
+    the finite results are below 64 and rounded to 8 or 11 bits; their sums are
+    good to 1e-3 in any order."""
+    gen = torch.Generator(device="cuda").manual_seed(m + rank)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    k, n, groups = 72, 72, 3
+    x, a, b = r(m, k), r(groups, rank, k) / k ** 0.5, r(groups, n, rank) / rank ** 0.5
+    a[0, :, 5] = a[0, :, 5].abs() + 0.1           # all of x[., 5]'s products have its sign
+    b[0, :24], b[0, 24:48] = b[0, :24].abs() + 0.01, -b[0, 24:48].abs() - 0.01
+    a[1, 3, 7] = float("inf")
+    a[2] = float("nan")
+    b[1] = torch.where(b[1].abs() < 0.01, 0.01, b[1])
+    ids = torch.arange(m, device="cuda", dtype=torch.int32) % groups
+    x[0, 5] = float("inf")
+    if m > 9:
+        x[3, 5], x[6, 11], x[9, 5] = float("-inf"), float("nan"), 1.0
+    x, a, b = x.to(DTYPES[dt]), a.to(DTYPES[dt]), b.to(DTYPES[dt])
+    got = sq.lora(x, a, b, sq.route(ids, groups))
+    for g in (0, 1, 2):
+        at = torch.nonzero(ids == g).flatten()
+        at = torch.cat([at[:40], at[-40:]])
+        if at.numel():
+            _same(got[at], _formula(x[at], a[g], b[g]), 2.0 ** (-8 if dt == "bf16" else -11) + 1e-3)
+    rows = torch.ones(m, dtype=torch.bool, device="cuda")
+    rows[0] = False
+    if m > 9:
+        rows[3] = rows[6] = False
+    assert bool(got[rows & (ids == 0)].isfinite().all())
+    assert sq.get_last_error() == sq.OK
+
+
+@pytest.mark.parametrize("m,rank", FORMS)
+def test_the_largest_finite_products(m, rank):
+    """bf16: x A^T that rounds to infinity in 16 bits but not in 32."""
+    x = torch.zeros(m, 64, dtype=torch.bfloat16, device="cuda")
+    x[:, 1], x[:, 9] = 2.0 ** 127, 1.5 * 2.0 ** 119
+    a = torch.zeros(1, rank, 64, dtype=torch.bfloat16, device="cuda")
+    a[0, 2, 1], a[0, 2, 9] = 255 / 128, 1.0
+    b = torch.zeros(1, 40, rank, dtype=torch.bfloat16, device="cuda")
+    b[0, :, 2] = 2.0 ** -100
+    got = sq.lora(x, a, b, sq.route(torch.zeros(m, dtype=torch.int32, device="cuda"), 1))
+    want = torch.full((m, 40), 255.75 * 2.0 ** 20, device="cuda").bfloat16()
+    assert torch.equal(got, want)
