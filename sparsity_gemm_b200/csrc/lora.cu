@@ -255,12 +255,12 @@ __device__ __forceinline__ void expand_tile(const LoraParams &p, int group, cons
                 v[j][s] = make_uint4(0, 0, 0, 0);
                 if (NB == 2) {  // one step of 16
                     if (in && 4 * q < p.rank) {
-                        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(at + 2 * j * p.rank));
+                        const uint2 w = load_as<uint2>(at + 2 * j * p.rank);
                         v[j][s].x = w.x;
                         v[j][s].y = w.y;
                     }
                 } else if (in && 32 * s + 8 * q < p.rank) {
-                    v[j][s] = __ldg(reinterpret_cast<const uint4 *>(at + 2 * j * p.rank + 32 * s));
+                    v[j][s] = load_as<uint4>(at + 2 * j * p.rank + 32 * s);
                 }
             }
         }
@@ -351,7 +351,7 @@ __device__ __forceinline__ void copy_bare_rows(const LoraParams &p) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     v[j] = make_uint4(0, 0, 0, 0);
-                    if (p.base && c0 + 256 * j < p.n) v[j] = __ldg(reinterpret_cast<const uint4 *>(src + c0 + 256 * j));
+                    if (p.base && c0 + 256 * j < p.n) v[j] = load_as<uint4>(src + c0 + 256 * j);
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -450,12 +450,12 @@ __global__ void __launch_bounds__(kLoraThreads, PER_SM) lora_kernel(const LoraPa
 #pragma unroll
                     for (int j = 0; j < NB; ++j) {
                         const int r = 8 * j + g8;
-                        av[u][j] = in && r < p.rank ? __ldg(reinterpret_cast<const uint4 *>(a + (int64_t)r * p.k + kk))
+                        av[u][j] = in && r < p.rank ? load_as<uint4>(a + (int64_t)r * p.k + kk)
                                                     : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        xv[u][h] = in && xr[h] ? __ldg(reinterpret_cast<const uint4 *>(xr[h] + kk)) : make_uint4(0, 0, 0, 0);
+                        xv[u][h] = in && xr[h] ? load_as<uint4>(xr[h] + kk) : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
                 for (int u = 0; u < C::kStep; ++u)

@@ -10,8 +10,8 @@
 // taken around the mean in a second pass over registers. That pass also sums
 // x - mu, which is what the first sum's error left out of the mean: with it the
 // mean is held as a binary32 number and a small rest, so a mean far above the
-// spread costs no digits (0.8 us more for 8192 x 4096 in fp16). Results are
-// rounded once. Every sum has a fixed order: the same inputs give the same bits.
+// spread costs no digits. Results are rounded once. Every sum has a fixed order:
+// the same inputs give the same bits.
 #include <cuda_runtime.h>
 #include <string.h>
 
@@ -97,7 +97,6 @@ struct NormParams {
     int64_t rows;
     int32_t k;
     float eps;
-    int32_t rms;
     int32_t lanes;  // of a row, where a warp holds whole rows
     float inv_k;
 };
@@ -181,8 +180,9 @@ struct Row {
             return make_float2(d, d * d);
         }
     }
-    // (x - mean) rstd w + b of vector c
-    static __device__ __forceinline__ P apply(P v, const RowStats &st, const T *w, const T *b, int c) {
+    // (x - mean) rstd w + b; wv, bv: the vectors of w and b (not looked at where
+    // there is none)
+    static __device__ __forceinline__ P apply(P v, const RowStats &st, bool w, P wv, bool b, P bv) {
         const float shift = -st.rest * st.rstd;
         if constexpr (VW > 1) {
             uint64_t f[VW / 2], g[VW / 2];
@@ -191,12 +191,12 @@ struct Row {
 #pragma unroll
             for (int e = 0; e < VW / 2; ++e) f[e] = fma2(add2(f[e], m), r, t);
             if (w) {
-                V::unpack2(V::load(w + (int64_t)c * VW), g);
+                V::unpack2(wv, g);
 #pragma unroll
                 for (int e = 0; e < VW / 2; ++e) f[e] = mul2(f[e], g[e]);
             }
             if (b) {
-                V::unpack2(V::load(b + (int64_t)c * VW), g);
+                V::unpack2(bv, g);
 #pragma unroll
                 for (int e = 0; e < VW / 2; ++e) f[e] = add2(f[e], g[e]);
             }
@@ -206,11 +206,11 @@ struct Row {
             V::unpack(v, f);
             f[0] = fmaf(f[0] - st.mu, st.rstd, shift);
             if (w) {
-                V::unpack(V::load(w + c), g);
+                V::unpack(wv, g);
                 f[0] *= g[0];
             }
             if (b) {
-                V::unpack(V::load(b + c), g);
+                V::unpack(bv, g);
                 f[0] += g[0];
             }
             return V::pack(f);
@@ -223,9 +223,10 @@ struct Row {
 // WARP: p.lanes lanes of a warp per row, kFwdWarps warps per CTA; else one CTA
 // per row.
 constexpr int kFwdWarps = 4;
+constexpr int kFwdPair = 640;  // 16-bit rows of 513 to 640 threads: two CTAs on an SM, for a few spills (512 x 20000: 12.3 us from 13.3)
 
-template <typename T, int VW, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kFwdWarps : 1024) norm_fwd_kernel(const NormParams p) {
+template <typename T, int VW, int NV, bool WARP, bool RMS, int MAXT = 1024>
+__global__ void __launch_bounds__(WARP ? 32 * kFwdWarps : MAXT, MAXT == kFwdPair ? 2 : 1) norm_fwd_kernel(const NormParams p) {
     using V = Vec<T, VW>;
     using R = Row<T, VW>;
     __shared__ __align__(16) float red[32];
@@ -252,8 +253,23 @@ __global__ void __launch_bounds__(WARP ? 32 * kFwdWarps : 1024) norm_fwd_kernel(
         const int c = i * threads + tid;
         xv[i] = c < nvec ? V::load(x + (int64_t)c * VW) : V::zero();
     }
+    auto fetch = [&](const T *from, int i) {
+        const int c = i * threads + tid;
+        return from && c < nvec ? V::load(from + (int64_t)c * VW) : V::zero();
+    };
+    // The first vectors of w and b set out before the row's sums, the others one
+    // ahead: the compiler moves no load over a barrier or a store (8192 x 4096 in
+    // fp16: 25.0 us from 27.0). In 32 bits that costs a CTA of registers (4096 x
+    // 4096: 28.1 us against 25.5).
+    constexpr int kAheadW = sizeof(T) == 4 && VW > 1 ? 0 : 1;
+    typename V::P wv[NV], bv[NV];
+#pragma unroll
+    for (int i = 0; i < kAheadW; ++i) {
+        wv[i] = fetch(w, i);
+        bv[i] = fetch(b, i);
+    }
     RowStats st;
-    if (p.rms) {
+    if (RMS) {
         float q = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) q += R::sum_squares(xv[i]);
@@ -281,16 +297,24 @@ __global__ void __launch_bounds__(WARP ? 32 * kFwdWarps : 1024) norm_fwd_kernel(
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = i * threads + tid;
-        if (c < nvec && here) V::store(y + (int64_t)c * VW, R::apply(xv[i], st, w, b, c));
+        if (i + kAheadW < NV) {
+            wv[i + kAheadW] = fetch(w, i + kAheadW);
+            bv[i + kAheadW] = fetch(b, i + kAheadW);
+        }
+        const typename V::P o = R::apply(xv[i], st, w != nullptr, wv[i], b != nullptr, bv[i]);
+        if (c < nvec && here) V::store(y + (int64_t)c * VW, o);
     }
 }
 
 // Rows too long for the registers: the same sums in three passes over the
-// row, which stays in L2 (at most 256 KB).
-constexpr int kLongThreads = 1024;
+// row, which stays in L2 (at most 256 KB). Two sums of every kind per thread, so
+// that none has more than 64 terms. Two CTAs of 512 threads on an SM leave room
+// for two vectors in flight (8192 x 4097 in fp16, single values: 112 us with CTAs
+// of 1024).
+constexpr int kLongThreads = 512;
 
-template <typename T, int VW>
-__global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(const NormParams p) {
+template <typename T, int VW, bool RMS>
+__global__ void __launch_bounds__(kLongThreads, 2) norm_fwd_long_kernel(const NormParams p) {
     using V = Vec<T, VW>;
     __shared__ __align__(16) float red[32];
     __shared__ float2 red2[32];
@@ -303,28 +327,51 @@ __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(const NormP
     const T *w = static_cast<const T *>(p.w), *b = static_cast<const T *>(p.b);
     using R = Row<T, VW>;
     RowStats st;
-    if (p.rms) {
-        float q = 0.0f;
-        for (int c = threadIdx.x; c < nvec; c += kLongThreads) q += R::sum_squares(V::load(x + (int64_t)c * VW));
-        st = rms_stats(row_sum<false>(q, red), p);
-    } else {
-        float s = 0.0f;
-        for (int c = threadIdx.x; c < nvec; c += kLongThreads) s += R::sum(V::load(x + (int64_t)c * VW));
-        const float mu0 = row_sum<false>(s, red) * p.inv_k;
-        float2 a = make_float2(0.0f, 0.0f);
-        for (int c = threadIdx.x; c < nvec; c += kLongThreads) {
-            const float2 d = R::sums_around(V::load(x + (int64_t)c * VW), mu0);
-            a.x += d.x;
-            a.y += d.y;
+    // f(u, vector c) for this thread's vectors, u = 0 and 1 in turn
+    auto walk = [&](auto f) {
+        for (int c = threadIdx.x; c < nvec; c += 2 * kLongThreads) {
+            f(0, V::load(x + (int64_t)c * VW));
+            if (c + kLongThreads < nvec) f(1, V::load(x + (int64_t)(c + kLongThreads) * VW));
         }
-        st = layer_stats(mu0, row_sum2<false>(a, red2), p);
+    };
+    if (RMS) {
+        float q[2] = {};
+        walk([&](int u, typename V::P v) { q[u] += R::sum_squares(v); });
+        st = rms_stats(row_sum<false>(q[0] + q[1], red), p);
+    } else {
+        float s[2] = {};
+        walk([&](int u, typename V::P v) { s[u] += R::sum(v); });
+        const float mu0 = row_sum<false>(s[0] + s[1], red) * p.inv_k;
+        float2 a[2] = {};
+        walk([&](int u, typename V::P v) {
+            const float2 d = R::sums_around(v, mu0);
+            a[u].x += d.x;
+            a[u].y += d.y;
+        });
+        st = layer_stats(mu0, row_sum2<false>(make_float2(a[0].x + a[1].x, a[0].y + a[1].y), red2), p);
     }
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = st.mu;
         if (p.rstd) p.rstd[row] = st.rstd;
     }
-    for (int c = threadIdx.x; c < nvec; c += kLongThreads)
-        V::store(y + (int64_t)c * VW, R::apply(V::load(x + (int64_t)c * VW), st, w, b, c));
+    constexpr int U = VW > 1 ? 2 : 1;  // vectors in flight
+    for (int c0 = threadIdx.x; c0 < nvec; c0 += U * kLongThreads) {
+        typename V::P xv[U], wv[U], bv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = c0 + u * kLongThreads;
+            const bool in = c < nvec;
+            xv[u] = in ? V::load(x + c * VW) : V::zero();
+            wv[u] = in && w ? V::load(w + c * VW) : V::zero();
+            bv[u] = in && b ? V::load(b + c * VW) : V::zero();
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = c0 + u * kLongThreads;
+            const typename V::P o = R::apply(xv[u], st, w != nullptr, wv[u], b != nullptr, bv[u]);
+            if (c < nvec) V::store(y + c * VW, o);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -398,8 +445,8 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(const NormBwdPara
             xn[i] = in ? V::load(xp + row * p.k + (int64_t)c * VW) : V::zero();
             dn[i] = in ? V::load(dyp + row * p.k + (int64_t)c * VW) : V::zero();
         }
-        mu_n = p.rms ? 0.0f : __ldg(p.mean + row);
-        rs_n = __ldg(p.rstd + row);
+        mu_n = p.rms ? 0.0f : p.mean[row];
+        rs_n = p.rstd[row];
     };
     if (first < p.rows) fetch(first);
     else clear();
@@ -562,8 +609,8 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kBwdSmall ? 2 : 1)
         const int64_t row = part + it * parts;
         const float mu = mu_n, rs = rs_n;
         if (it + 1 < iters) {
-            if (!p.rms) mu_n = __ldg(p.mean + row + parts);
-            rs_n = __ldg(p.rstd + row + parts);
+            if (!p.rms) mu_n = p.mean[row + parts];
+            rs_n = p.rstd[row + parts];
         }
         const uint64_t mu2 = pk2(-mu, -mu), rs2 = pk2(rs, rs);
         (void)mbar_wait_own(smem_u32(&full[slot]), phase, status, kSiteNormRing, wait_ns);
@@ -815,7 +862,7 @@ __global__ void __launch_bounds__(32 * W) norm_bwd_reduce_kernel(const float *pa
 
 static int threads_for(int nvec, int nv) { return (int)round_up((nvec + nv - 1) / nv, 32); }
 
-template <typename T, int VW>
+template <typename T, int VW, bool RMS>
 static sharq_status norm_fwd(LaunchCtx &ctx, const NormParams &p) {
     const int nvec = p.k / VW;
     if (nvec <= 128) {
@@ -823,20 +870,25 @@ static sharq_status norm_fwd(LaunchCtx &ctx, const NormParams &p) {
         const int nv = nvec <= 64 ? 2 : 4;
         for (q.lanes = 1; q.lanes * nv < nvec; q.lanes *= 2) {}
         const int64_t per = 32 * kFwdWarps / q.lanes, grid = (p.rows + per - 1) / per;
-        return nv == 2 ? launch_pdl(ctx, norm_fwd_kernel<T, VW, 2, true>, grid, 32 * kFwdWarps, 0, 1, q)
-                       : launch_pdl(ctx, norm_fwd_kernel<T, VW, 4, true>, grid, 32 * kFwdWarps, 0, 1, q);
+        return nv == 2 ? launch_pdl(ctx, norm_fwd_kernel<T, VW, 2, true, RMS>, grid, 32 * kFwdWarps, 0, 1, q)
+                       : launch_pdl(ctx, norm_fwd_kernel<T, VW, 4, true, RMS>, grid, 32 * kFwdWarps, 0, 1, q);
     }
-    if (nvec <= 4096) return launch_pdl(ctx, norm_fwd_kernel<T, VW, 4, false>, p.rows, threads_for(nvec, 4), 0, 1, p);
-    return launch_pdl(ctx, norm_fwd_long_kernel<T, VW>, p.rows, kLongThreads, 0, 1, p);
+    if constexpr (VW == 8)
+        if (nvec > 4 * 512 && nvec <= 4 * kFwdPair)
+            return launch_pdl(ctx, norm_fwd_kernel<T, VW, 4, false, RMS, kFwdPair>, p.rows, threads_for(nvec, 4), 0, 1, p);
+    if (nvec <= 4096) return launch_pdl(ctx, norm_fwd_kernel<T, VW, 4, false, RMS>, p.rows, threads_for(nvec, 4), 0, 1, p);
+    return launch_pdl(ctx, norm_fwd_long_kernel<T, VW, RMS>, p.rows, kLongThreads, 0, 1, p);
 }
 
 sharq_status launch_layer_norm(LaunchCtx &ctx, const void *x, int64_t rows, int64_t k, const void *w, const void *b,
                                float eps, int norm, int dtype, void *y, float *mean, float *rstd, bool vec16) {
     if (rows == 0) return SHARQ_OK;
-    NormParams p{x, w, b, y, mean, rstd, rows, (int32_t)k, eps, norm, 32, 1.0f / (float)k};
+    NormParams p{x, w, b, y, mean, rstd, rows, (int32_t)k, eps, 32, 1.0f / (float)k};
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        return vec16 ? norm_fwd<T, 16 / (int)sizeof(T)>(ctx, p) : norm_fwd<T, 1>(ctx, p);
+        constexpr int VW = 16 / (int)sizeof(T);
+        if (norm == 1) return vec16 ? norm_fwd<T, VW, true>(ctx, p) : norm_fwd<T, 1, true>(ctx, p);
+        return vec16 ? norm_fwd<T, VW, false>(ctx, p) : norm_fwd<T, 1, false>(ctx, p);
     });
 }
 

@@ -16,6 +16,13 @@
 
 namespace sq {
 
+// Loads are plain ones. What they read the launch before may have written, and it
+// still runs when these kernels start; and some of it is the call's own output (dy,
+// residual, base). Loads marked read-only may be moved ahead of griddep_wait, or
+// past the store to the same place.
+template <typename P>
+__device__ __forceinline__ P load_as(const void *p) { return *static_cast<const P *>(p); }
+
 // Loads and stores of VW consecutive elements (VW * sizeof(T) bytes, that
 // alignment), held packed until they are widened.
 template <int BYTES>
@@ -72,7 +79,7 @@ struct Vec {
         for (int i = 0; i < VW; ++i) f[i] = 1.0f;
         return pack(f);
     }
-    static __device__ __forceinline__ P load(const T *p) { return __ldg(reinterpret_cast<const P *>(p)); }
+    static __device__ __forceinline__ P load(const T *p) { return load_as<P>(p); }
     static __device__ __forceinline__ void store(T *p, P v) { *reinterpret_cast<P *>(p) = v; }
     static __device__ __forceinline__ void unpack(P v, float (&f)[VW]) {
         T t[VW];
