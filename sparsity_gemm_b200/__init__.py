@@ -17,6 +17,7 @@ import os
 
 import numpy as np
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsharq.so")
@@ -598,12 +599,17 @@ def _take(t, name: str, dev: int, dtype, shape, rows: bool = False):
 
 def _no_grad(*ts):
     """The calls below are not recorded by autograd; a call that would lose a
-    gradient silently, or write to a tensor that wants one, is refused (the
-    *_backward calls are the gradients)."""
-    for t in ts:
-        if t is not None and t.requires_grad:
-            raise ValueError("tensors that require a gradient are refused: call under torch.no_grad() and use the "
-                             "backward calls")
+    gradient or a forward-mode tangent silently, or write to a tensor that has
+    or wants one, is refused (the *_backward calls are the gradients)."""
+    if torch.is_grad_enabled():
+        for t in ts:
+            if t is not None and t.requires_grad:
+                raise ValueError("tensors that require a gradient are refused: call under torch.no_grad() and use the "
+                                 "backward calls")
+    if forward_ad._current_level >= 0:  # inside dual_level(), which no_grad() does not end
+        for t in ts:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("tensors that carry a forward-mode tangent are refused: it would be lost")
 
 
 def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
@@ -655,8 +661,7 @@ def layer_norm(x: torch.Tensor, w=None, b=None, eps: float = 1e-5, norm: str = "
     if b is not None:
         _require(kind == 0, "RMSNorm takes no b")
         _take(b, "b", dev, dt, (k,))
-    if torch.is_grad_enabled():
-        _no_grad(x, w, b, out)
+    _no_grad(x, w, b, out)
     if out is None:
         out = _new_like(x, stream)
     else:
@@ -694,8 +699,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean, rstd: torch.Ten
     _take(rstd, "rstd", dev, _f32, (m_tok,))
     if w is not None:
         _take(w, "w", dev, dt, (k,))
-    if torch.is_grad_enabled():
-        _no_grad(dy, x, w, out)
+    _no_grad(dy, x, mean, rstd, w, out)
     if out is None:
         out = _new_like(x, stream)
     else:
@@ -771,8 +775,7 @@ def permute_rows(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = N
     _routing(routing, dev)
     m_tok, k = x.shape
     _require(routing.m_tok == m_tok, "routing is of another number of tokens")
-    if torch.is_grad_enabled():
-        _no_grad(x, out)
+    _no_grad(x, out)
     shape = (m_tok * routing.top_k, k)
     if out is None:
         out = _new(x, shape, x.dtype, stream)
@@ -799,8 +802,7 @@ def combine(y: torch.Tensor, routing: Routing, weights: torch.Tensor | None = No
         _take(weights, "weights", dev, _f32, (m_tok, top_k))
     if residual is not None:
         _take(residual, "residual", dev, dt, (m_tok, k))
-    if torch.is_grad_enabled():
-        _no_grad(y, weights, residual, out)
+    _no_grad(y, weights, residual, out)
     if out is None:
         out = _new(y, (m_tok, k), dt, stream)
     else:
@@ -823,8 +825,7 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, routing: Routing, weig
     rows, k = y.shape
     _take(dout, "dout", dev, dt, (m_tok, k))
     _take(weights, "weights", dev, _f32, (m_tok, top_k))
-    if torch.is_grad_enabled():
-        _no_grad(dout, y, weights)
+    _no_grad(dout, y, weights)
     dy = _new_like(y, stream)
     dweights = _new_like(weights, stream)
     st = (_lib or lib()).sharq_combine_backward(dout.data_ptr(), y.data_ptr(), rows, m_tok, k, routing.slots.data_ptr(),
@@ -871,8 +872,7 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, routing: Routing, sc
     if base is not None:
         _take(base, "base", dev, dt, (m_tok, n_out), True)
         ldbase = base.stride(0) if m_tok > 1 else n_out
-    if torch.is_grad_enabled():
-        _no_grad(x, a, b, scales, base, out)
+    _no_grad(x, a, b, scales, base, out)
     if out is None:
         out = _new(x, (m_tok, n_out), dt, stream)
         ldo = n_out
