@@ -692,8 +692,10 @@ sharq_status sharq_get_last_error(void *stream);
  * Valid after sharq_get_last_error returned one of them. */
 uint32_t sharq_last_timeout_site(void);
 
-/* Test hook: the wait limit of the GEMM's bounded waits, in nanoseconds
- * (default 2e9). 0 restores the default. Returns the previous value. */
+/* Test hook: the limit of the kernels' bounded waits (the GEMMs', and those of
+ * the norm gradient and the adapters), in nanoseconds (default 2e9). 0 restores
+ * the default. Returns the previous value. A call whose wait runs out leaves
+ * its outputs unspecified and reports SHARQ_ERR_TIMEOUT. */
 uint64_t sharq_set_wait_limit_ns(uint64_t ns);
 
 /* Failure-detection self-test: enqueues one CTA whose single thread waits,

@@ -581,9 +581,9 @@ __global__ void __launch_bounds__(kShThreads, ShrinkCfg<R>::kPerSm)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap tm_a, const LoraParams p) {
     using C = ShrinkCfg<R>;
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], made[2], taken[2];
+    __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], made[2], taken[2], drained;
     __shared__ uint32_t tmem_s;
-    __shared__ int table_ok;
+    __shared__ int table_ok, gave_up;  // gave_up: a role's wait ran out
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = (smem_u32(dyn) + 1023u) & ~1023u;
     int32_t *off = reinterpret_cast<int32_t *>(dyn + (ring - smem_u32(dyn)) + C::kStages * C::kStage);  // [groups + 1]
@@ -601,6 +601,8 @@ __global__ void __launch_bounds__(kShThreads, ShrinkCfg<R>::kPerSm)
             mbar_init(smem_u32(&made[a]), 1);
             mbar_init(smem_u32(&taken[a]), kShWriters);
         }
+        mbar_init(smem_u32(&drained), 1);
+        gave_up = 0;
         mbar_fence_init();
     }
     tc_fence_before();
@@ -627,10 +629,14 @@ __global__ void __launch_bounds__(kShThreads, ShrinkCfg<R>::kPerSm)
         for (int64_t w = w0; w < w1; ++n) {
             const int tile = (int)(w / share.blocks), b0 = (int)(w % share.blocks);
             const int b1 = (int)min((int64_t)share.blocks, b0 + w1 - w);
-            if (!f(n, tile, group_of_tile(tiles, p.groups, tile), b0, b1)) return;
+            if (!f(n, tile, group_of_tile(tiles, p.groups, tile), b0, b1)) {
+                gave_up = 1;
+                return;
+            }
             w += b1 - b0;
         }
     };
+    int fills = 0;  // stages that the thread of A's copies has set out
     if (warp < 4) {
         // 16-byte copies into the products' layout (128-byte rows, piece c of
         // row r at c ^ (r % 8)): 8 threads per row, every 16th row. Rows past
@@ -666,16 +672,11 @@ __global__ void __launch_bounds__(kShThreads, ShrinkCfg<R>::kPerSm)
         cp_async_wait<0>();
     } else if (warp == 4) {
         if (lane == 0) {
-            int i = 0;
             parts([&](int, int, int group, int b0, int b1) {
-                for (int b = b0; b < b1; ++b, ++i) {
-                    const int s = i % C::kStages;
-                    if (!mbar_wait_own(smem_u32(&empty[s]), ((i / C::kStages) & 1) ^ 1, p.status, kSiteLoraEmpty, p.wait_ns)) {
-                        // gave up: let the copies in flight land before the CTA's shared memory goes
-                        for (int f = i < C::kStages ? 0 : i - C::kStages; f < i; ++f)
-                            (void)mbar_wait_own(smem_u32(&full[f % C::kStages]), (f / C::kStages) & 1, nullptr, 0, 10000000ull);
+                for (int b = b0; b < b1; ++b, ++fills) {
+                    const int s = fills % C::kStages;
+                    if (!mbar_wait_own(smem_u32(&empty[s]), ((fills / C::kStages) & 1) ^ 1, p.status, kSiteLoraEmpty, p.wait_ns))
                         return false;
-                    }
                     const uint32_t bar = smem_u32(&full[s]);
                     mbar_arrive_expect_tx(bar, R * kShK * 2);
                     tma_load_2d(ring + s * C::kStage + kShX, &tm_a, b * kShK, group * p.rank, bar);
@@ -736,6 +737,19 @@ __global__ void __launch_bounds__(kShThreads, ShrinkCfg<R>::kPerSm)
         tc_fence_before();
     }
     __syncthreads();
+    if (gave_up) {
+        // A's copies and the products in flight end before the CTA's shared and
+        // tensor memory go (a copier waited for its own above)
+        if (warp == 4 && lane == 0)
+            for (int f = fills < C::kStages ? 0 : fills - C::kStages; f < fills; ++f)
+                (void)mbar_wait_own(smem_u32(&full[f % C::kStages]), (f / C::kStages) & 1, nullptr, 0, kOwnDrainNs);
+        if (warp == 5 && lane == 0) {
+            tc_commit(smem_u32(&drained));
+            (void)mbar_wait_own(smem_u32(&drained), 0, nullptr, 0, kOwnDrainNs);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
     tc_fence_after();
     if (warp == 5) tmem_dealloc(tmem, C::kTmem);
 }

@@ -566,6 +566,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kBwdSmall ? 2 : 1)
     extern __shared__ __align__(128) uint8_t ring[];  // [stages][x, dy][part of a row]
     __shared__ uint64_t full[kRingMax];
     __shared__ __align__(16) float2 red[2][MAXT / 32];
+    __shared__ int gave_up[2];  // a wait of this row ran out (rows take turns, as in red)
     griddep_wait();
     griddep_launch();
     const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5, lane = tid & 31;
@@ -586,6 +587,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kBwdSmall ? 2 : 1)
     if (tid == 0) {
         for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&full[s]), 1);
         mbar_fence_init();
+        gave_up[0] = gave_up[1] = 0;
     }
     if (tid < 2 * (MAXT / 32)) red[tid / (MAXT / 32)][tid % (MAXT / 32)] = make_float2(0.0f, 0.0f);  // warps not there
     __syncthreads();
@@ -613,7 +615,8 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kBwdSmall ? 2 : 1)
             rs_n = p.rstd[row + parts];
         }
         const uint64_t mu2 = pk2(-mu, -mu), rs2 = pk2(rs, rs);
-        (void)mbar_wait_own(smem_u32(&full[slot]), phase, status, kSiteNormRing, wait_ns);
+        const int parity = it & 1;
+        if (!mbar_wait_own(smem_u32(&full[slot]), phase, status, kSiteNormRing, wait_ns)) gave_up[parity] = 1;
         uint64_t h[NV][H], g[NV][H], t1 = 0, t2 = 0;  // xhat and g = dy w; sums of g and g xhat
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -639,10 +642,15 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kBwdSmall ? 2 : 1)
         float v = (lane & 16 ? s2 : s1) + __shfl_xor_sync(0xFFFFFFFFu, lane & 16 ? s1 : s2, 16);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        const int parity = it & 1;
         if (lane == 0) red[parity][warp].x = v;
         if (lane == 16) red[parity][warp].y = v;
         __syncthreads();
+        if (gave_up[parity]) {  // the copies in flight land before the CTA's shared memory goes
+            if (tid == 0)
+                for (int f = it; f < iters && f < it + stages; ++f)
+                    (void)mbar_wait_own(smem_u32(&full[f % stages]), (f / stages) & 1, nullptr, 0, kOwnDrainNs);
+            return;
+        }
         if (tid == 0 && it + stages < iters) issue(it + stages, slot);
         s1 = s2 = 0.0f;
         const float4 *rp = reinterpret_cast<const float4 *>(red[parity]);

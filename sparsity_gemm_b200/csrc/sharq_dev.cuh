@@ -395,6 +395,10 @@ __device__ __forceinline__ bool mbar_wait_own(uint32_t bar, uint32_t parity, uns
     }
 }
 
+// How long a kernel that gave up waits for each of its own copies and products
+// in flight, before it returns.
+constexpr uint64_t kOwnDrainNs = 10000000ull;
+
 // Wait sites of the 16/32-bit operators.
 enum : unsigned { kSiteNormRing = 0x141, kSiteLoraFull = 0x142, kSiteLoraEmpty = 0x143, kSiteLoraDone = 0x144,
                 kSiteLoraTaken = 0x145 };
