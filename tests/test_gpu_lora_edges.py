@@ -108,3 +108,70 @@ def test_the_largest_finite_products(m, rank):
     got = sq.lora(x, a, b, sq.route(torch.zeros(m, dtype=torch.int32, device="cuda"), 1))
     want = torch.full((m, 40), 255.75 * 2.0 ** 20, device="cuda").bfloat16()
     assert torch.equal(got, want)
+
+
+# (rows, rank, adapters) of both forms, the two-launch one with padded ranks and
+# with tiles that end early
+BOTH = [(30, 16, 3), (100, 24, 5), (1100, 72, 3), (2700, 24, 4), (3600, 8, 3), (130, 64, 200)]
+
+
+def _adapter_case(m, rank, groups, dt, none):
+    gen = torch.Generator(device="cuda").manual_seed(m + rank)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda").to(dt)  # noqa: E731
+    k, n = 136, 72
+    ids = torch.randint(0, groups, (m,), generator=gen, device="cuda", dtype=torch.int32)
+    ids[torch.rand(m, generator=gen, device="cuda") < none] = -1
+    return r(m, k), r(groups, rank, k) / k ** 0.5, r(groups, n, rank) / rank ** 0.5, r(m, n), ids
+
+
+@pytest.mark.parametrize("m,rank,groups", BOTH)
+def test_bad_routing_is_reported_in_both_forms(m, rank, groups):
+    x, a, b, base, ids = _adapter_case(m, rank, groups, torch.float16, 0.1)
+    r = sq.route(ids, groups)
+    good = sq.lora(x, a, b, r, base=base)
+    assert sq.get_last_error() == sq.OK
+    total = int(r.offsets[-1])
+    bare = ids < 0
+    edits = [(0, 1), (-1, m + 1), (1, -5), (1, total + 7 if groups > 1 else m + 7)]
+    for at, value in edits:
+        offsets = r.offsets.clone()
+        offsets[at] = value
+        out = torch.full_like(base, 7.0)
+        sq.lora(x, a, b, sq.Routing(offsets, r.rows, r.slots), base=base, out=out)
+        assert sq.get_last_error() == sq.ERR_INVALID_ARG
+        assert bool((out[~bare] == 7.0).all()) and torch.equal(out[bare], base[bare])
+    for bad in (m, m + 100, -1, -(2 ** 31)):  # rows out of range are left out, the others are as before
+        rows = r.rows.clone()
+        at = torch.tensor([0, total // 2, total - 1], device="cuda")
+        lost = rows[at].long()
+        rows[at] = bad
+        out = torch.full_like(base, 7.0)
+        sq.lora(x, a, b, sq.Routing(r.offsets, rows, r.slots), base=base, out=out)
+        assert sq.get_last_error() == sq.ERR_INVALID_ARG
+        keep = torch.ones(m, dtype=torch.bool, device="cuda")
+        keep[lost] = False
+        assert torch.equal(out[keep], good[keep]) and bool((out[lost] == 7.0).all())
+    assert torch.equal(sq.lora(x, a, b, r, base=base), good) and sq.get_last_error() == sq.OK
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("m,rank,groups", BOTH)
+def test_nothing_leaks_between_adapters_and_rows(m, rank, groups, dt):
+    """NaN and infinity in every second adapter (behind the padded rank of the
+    one before it) and in the last rows of a group: the rows of the others keep
+    their bits."""
+    x, a, b, base, ids = _adapter_case(m, rank, groups, DTYPES[dt], 0.1)
+    r = sq.route(ids, groups)
+    good = sq.lora(x, a, b, r, base=base)
+    clean = (ids < 0) | (ids % 2 == 0)
+    ends = r.offsets[1:][r.offsets[1:] > r.offsets[:-1]].long() - 1  # each group's last grouped row
+    last = r.rows[ends].long()
+    x[last[0::2]] = float("nan")
+    x[last[1::2]] = float("inf")
+    clean[last] = False
+    clean |= ids < 0
+    a[1::2, 0], a[1::2, -1], b[1::2] = float("nan"), float("inf"), float("nan")
+    got = sq.lora(x, a, b, r, base=base)
+    assert torch.equal(got[clean], good[clean])
+    assert bool(got[last].isnan().any(1).all())
+    assert sq.get_last_error() == sq.OK
