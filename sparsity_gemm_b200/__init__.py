@@ -749,7 +749,9 @@ def _routing(r, dev: int):
 def route(ids: torch.Tensor, groups: int, stream=None) -> Routing:
     """Entries sorted by group, on the GPU: ids [m_tok, top_k] (or [m_tok]),
     int32 or int64, holds each entry's expert or adapter; an id outside 0 ..
-    groups - 1 (-1, say) means none. Entries of a group keep their order."""
+    groups - 1 (-1, say) means none. Entries of a group keep their order.
+    gather_rows, prepare_grouped and linear_grouped want every row in a group
+    (offsets[-1] rows): where entries have none, give them rows[:offsets[-1]]."""
     _require(isinstance(ids, torch.Tensor) and ids.dtype in (_i32, torch.int64) and ids.dim() in (1, 2),
              "ids must be an int32 or int64 matrix (or vector)")
     dev = _first(ids, "ids", ids.dim(), False, ids.dtype)
@@ -769,8 +771,9 @@ def route(ids: torch.Tensor, groups: int, stream=None) -> Routing:
 
 def permute_rows(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Rows of x [m_tok, k] in grouped order: [m_tok * top_k, k], row
-    slots[t, j] = x[t], zero behind the last group (what prepare_grouped and
-    the grouped products read). Its gradient is combine(dy, routing)."""
+    slots[t, j] = x[t], zero behind the last group: the input of experts in 16
+    or 32 bits (for the FP4 ones gather_rows moves prepared rows, each token
+    prepared once). Its gradient is combine(dy, routing)."""
     dev = _first(x, "x")
     _routing(routing, dev)
     m_tok, k = x.shape
@@ -849,8 +852,8 @@ def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, routing: Routing, sc
       x [m_tok, k], a [adapters, rank, k], b [adapters, n_out, rank] (fp16 or
       bf16; k, n_out and rank multiples of 8, rank <= 128); routing: route of
       the rows' adapters ([m_tok] or [m_tok, 1]); scales fp32 [adapters].
-    base is the shared projection's output, e.g. linear()'s; out may be base
-    itself, and x, base and out may be column slices (rows strided)."""
+    base is the shared projection's output in x's type, e.g. linear()'s (fp16);
+    out may be base itself, and x, base and out may be column slices (rows strided)."""
     dev = _first(x, "x", 2, True)
     dt = x.dtype
     _require(dt != _f32, "x must be an fp16 or bf16 matrix")
