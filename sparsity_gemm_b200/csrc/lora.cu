@@ -922,15 +922,18 @@ static sharq_status lora_two(LaunchCtx &ctx, LoraParams p) {
 
 // Whether a call takes the two-launch form (and so needs a workspace), by what
 // the host knows: rows, rank and adapters (not how many of them the batch
-// uses). Measured at k = n = 4096 in fp16, one launch against two, in us:
+// uses). Measured at k = n = 4096 in fp16, one launch against two, in us, rows
+// shared evenly among the adapters:
 //   rank 16   1 adapter:           1024 rows 12 / 14, 3000 22 / 23, 4096 40 / 29
 //             64 adapters:         1024 13 / 21, 3000 24 / 27, 4096 41 / 32
-//   rank 32   1 adapter:           2048 18 / 22, 3000 34 / 26; 64: 2048 20 / 26, 3000 38 / 32
-//   rank 64   1 adapter:           64 10 / 11, 1024 17 / 19, 1500 29 / 23, 4096 58 / 44
+//   rank 32   1 adapter:           2048 18 / 21, 3000 34 / 26; 64: 2048 20 / 26, 3000 38 / 32
+//   rank 64   1 adapter:           64 10 / 11, 1024 17 / 19, 1500 30 / 23, 4096 64 / 43
 //             64 adapters:         64 17 / 26, 1024 23 / 31, 1500 38 / 33
 //             64 used of 256:      64 19 / 28, 256 31 / 29, 1024 38 / 32
-//   rank 128  1 adapter:           1024 26 / 28, 1500 50 / 34
+//   rank 128  1 adapter:           1024 27 / 27, 1500 55 / 33
 //             100 used of 256:     128 74 / 65, 1024 80 / 70
+// Shared at random, groups end in more tiles (64 adapters, rank 64, 1024 rows: 41
+// / 32). The third term in bf16 costs both forms alike.
 // One launch leads as long as its 16-row tiles fit on the GPU at once; their
 // accumulators and reading A and B per 16 rows cost more the larger the rank is.
 static bool lora_many(int64_t m, int64_t rank, int64_t groups) {
